@@ -56,6 +56,8 @@ SIGNATURES = {
     "nvfp4_quantize_delayed": (_int, [_vp, _i64, _i64, _vp, _i32, ctypes.c_uint32, _int, _u64, _u64,
                                       _vp, _vp, _vp, _vp]),
     "fp8_quantize_128x128": (_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
+    "fp8_matmul": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _int, _vp, _i32, _vp, _int, _vp,
+                          _vp]),
     "mxfp4_dequantize_rows": (_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
     "mxfp4_scales_mma_bytes": (_i64, [_i64, _i64]),
     "mxfp4_scales_mma_layout": (_int, [_vp, _i64, _i64, _vp, _vp]),
@@ -413,6 +415,59 @@ def fp8_quantize_1x128(x: torch.Tensor, y=None, s=None):
 def fp8_quantize_128x128(w: torch.Tensor, y=None, s=None):
     """BF16 [N, K] -> (E4M3 codes uint8 [N, K], float32 scales [N/128, K/128])."""
     return _fp8_blocks("fp8_quantize_128x128", w, 128, y, s)
+
+
+# ---------------------------------------------------------------- FP8 matrix products
+
+def _dev_status(dev_status):
+    if dev_status is not None:
+        _need(dev_status, torch.int32, "dev_status")
+        if dev_status.numel() < 1:
+            raise ValueError("dev_status must hold one int32")
+
+
+def _out_dtype(out, out_dtype, name="out"):
+    dt = out_dtype if out is None else out.dtype
+    if dt not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be bfloat16 or float32, got {dt}")
+    return dt
+
+
+def fp8_matmul(y: torch.Tensor, ys: torch.Tensor, w: torch.Tensor, ws: torch.Tensor,
+               group_offsets: torch.Tensor | None = None, out: torch.Tensor | None = None,
+               out_dtype: torch.dtype = torch.bfloat16, dev_status: torch.Tensor | None = None):
+    """E4M3 rows (y uint8 [M, K], ys float32 [M, K/128]) times E4M3 weights.
+
+    Dense: w uint8 [N, K].  Per expert: w uint8 [G, N, K] with int64 group
+    offsets [G+1] (device).  ws holds one scale per 128x128 tile ([...,
+    ceil(N/128), K/128]) or per 1x128 block ([..., N, K/128]).  Returns out
+    [M, N], BF16 or float32; rows past the last group are 0."""
+    _need(y, torch.uint8, "y", 2)
+    M, K = y.shape
+    _need(ys, torch.float32, "ys", 2, shape=(M, K // 128))
+    if group_offsets is None:
+        _need(w, torch.uint8, "w", 2)
+        G, lead = 1, ()
+    else:
+        G = _groups(group_offsets)
+        _need(w, torch.uint8, "w", 3)
+        lead = (G,)
+    N = w.shape[-2]
+    _need(w, torch.uint8, "w", shape=(*lead, N, K))
+    _need(ws, torch.float32, "ws")
+    tiles, rows = (*lead, (N + 127) // 128, K // 128), (*lead, N, K // 128)
+    if tuple(ws.shape) not in (tiles, rows):
+        raise ValueError(f"ws must have shape {tiles} or {rows}, got {tuple(ws.shape)}")
+    dt = _out_dtype(out, out_dtype)
+    out = _empty((M, N), dt, y) if out is None else out
+    _need(out, dt, "out", numel=M * N)
+    _dev_status(dev_status)
+    _on_device(y=y, ys=ys, w=w, ws=ws, group_offsets=group_offsets, out=out,
+               dev_status=dev_status)
+    _call("fp8_matmul", _p(y), _p(ys), M, K, _p(w), _p(ws), N,
+          128 if tuple(ws.shape) == tiles else 1, _p(group_offsets), G, _p(out),
+          int(dt == torch.float32), _p(dev_status), _stream())
+    return out
 
 
 def mxfp4_dequantize_rows(q: torch.Tensor, s: torch.Tensor, out: torch.Tensor | None = None):

@@ -214,6 +214,41 @@ fq_status fp8_quantize_128x128(const void *w, int64_t N, int64_t K, uint8_t *y, 
                                void *stream);
 
 /*
+ * Block-scaled FP8 matrix product ([MoE-FP4] 2.1: E4M3 operands with
+ * 128-element blocks and FP32 block scales; 2.3: ragged per-expert groups
+ * without padding), dense or per expert:
+ *   a  : uint8 [M, K]       E4M3 rows, sa: float [M, K/128] (1x128 blocks), as
+ *                           fp8_quantize_1x128 or fp4_to_fp8_rows write them
+ *   b  : uint8 [G, N, K]    E4M3 weights, one [N, K] matrix per group
+ *   sb : b_block = 128: float [G, ceil(N/128), K/128] (128x128 tiles, as
+ *        fp8_quantize_128x128 writes them); b_block = 1: float [G, N, K/128]
+ *   group_offsets : int64 [G+1] in device memory: group g owns the rows
+ *        offsets[g] .. offsets[g+1]-1 of a and c (offsets[0] = 0,
+ *        non-decreasing, offsets[G] <= M; empty groups allowed); NULL with
+ *        G = 1: all M rows
+ *   c  : [M, N] BF16 (c_f32 = 0) or FP32 (c_f32 = 1), output
+ *   c[m, n] = sum over the blocks t of K of  sa[m, t] sb[g, n, t] *
+ *             sum over k in t of  a[m, k] b[g, n, k]
+ * with the inner and the outer sum in binary32, rounded once to BF16 where
+ * c is BF16.  A NaN scale or code makes the outputs that it enters NaN.
+ * Rows offsets[G] .. M-1, which belong to no group, are written as 0.
+ * Forward: a = activations, b = weights; input gradient: a = output
+ * gradients, b = the codes and scales of the transposed weights.
+ *   dev_status : optional int32 in device memory: malformed offsets are
+ *        clamped (nothing is written out of bounds) and 1 is ORed into it; 2 is
+ *        ORed in if a wait inside the kernel ran out after two seconds (the
+ *        output is then incomplete; not expected to happen)
+ * Requires K > 0, K % 128 == 0, N > 0 (any N; N % 8 == 0 stores 16 bytes at a
+ * time), 0 <= M < 2^31 - 512, 1 <= G <= FQ_COLS_MAX_GROUPS.  Needs the
+ * driver's tensor-map encoder (FQ_ERR_CUDA with cudaErrorNotSupported
+ * otherwise).  Each output is one fixed sequence of operations: the same
+ * inputs give the same bits.
+ */
+fq_status fp8_matmul(const uint8_t *a, const float *sa, int64_t M, int64_t K, const uint8_t *b,
+                     const float *sb, int64_t N, int b_block, const int64_t *group_offsets,
+                     int32_t G, void *c, int c_f32, int32_t *dev_status, void *stream);
+
+/*
  * MXFP4 -> BF16 dequantization ([MoE-FP4] 2.1: an element's value is its
  * E2M1 value times 2^(e-127) of its block's UE8M0 scale byte e).
  *   q, s : MXFP4 [M, K/2], [M, K/32];  x : bf16 [M, K] (output)
