@@ -58,6 +58,15 @@ SIGNATURES = {
     "fp8_quantize_128x128": (_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
     "fp8_matmul": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _int, _vp, _i32, _vp, _int, _vp,
                           _vp]),
+    "fp8_quantize_cols": (_int, [_vp, _i64, _i64, _vp, _i32, _vp, _vp, _i64, _vp, _vp]),
+    "fp8_matmul_wgrad_workspace": (_i64, [_i64, _i64, _i64, _i32]),
+    "fp8_matmul_wgrad": (_int, [_vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _i32, _i64, _vp, _int,
+                                _int, _vp, _i64, _vp, _vp]),
+    "moe_route": (_int, [_vp, _int, _i64, _i32, _i32, _vp, _int, _i32, _i32, _i32, _int,
+                         ctypes.c_float, _vp, _vp, _vp]),
+    "moe_route_backward": (_int, [_vp, _int, _i64, _i32, _vp, _vp, _i32, _int, _int,
+                                  ctypes.c_float, _vp, _vp]),
+    "moe_sort_rows": (_int, [_vp, _i64, _i32, _vp, _vp, _vp, _vp]),
     "mxfp4_dequantize_rows": (_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
     "mxfp4_scales_mma_bytes": (_i64, [_i64, _i64]),
     "mxfp4_scales_mma_layout": (_int, [_vp, _i64, _i64, _vp, _vp]),
@@ -468,6 +477,150 @@ def fp8_matmul(y: torch.Tensor, ys: torch.Tensor, w: torch.Tensor, ws: torch.Ten
           128 if tuple(ws.shape) == tiles else 1, _p(group_offsets), G, _p(out),
           int(dt == torch.float32), _p(dev_status), _stream())
     return out
+
+
+def fp8_quantize_cols(x: torch.Tensor, group_offsets: torch.Tensor | None = None,
+                      yT: torch.Tensor | None = None, yT_scale: torch.Tensor | None = None,
+                      dev_status: torch.Tensor | None = None):
+    """BF16 [M, K] with int64 group offsets [G+1] (device; None: one group) ->
+    (yT uint8 [K, M] E4M3, yT_scale float32 [cap, K]: one row of K scales per
+    128-token block of a group, rows past the last block 0)."""
+    _bf16_2d(x, "x")
+    M, K = x.shape
+    G = 1 if group_offsets is None else _groups(group_offsets)
+    cap = fp4_to_fp8_cols_scale_capacity(M, G)
+    yT = _empty((K, M), torch.uint8, x) if yT is None else yT
+    yT_scale = _empty((cap, K), torch.float32, x) if yT_scale is None else yT_scale
+    _need(yT, torch.uint8, "yT", numel=K * M)
+    _need(yT_scale, torch.float32, "yT_scale", 2)
+    if yT_scale.shape[1] != K or yT_scale.shape[0] < cap:
+        raise ValueError(f"yT_scale must be [>= {cap}, {K}], got {tuple(yT_scale.shape)}")
+    _dev_status(dev_status)
+    _on_device(x=x, group_offsets=group_offsets, yT=yT, yT_scale=yT_scale, dev_status=dev_status)
+    _call("fp8_quantize_cols", _p(x), M, K, _p(group_offsets), G, _p(yT), _p(yT_scale),
+          int(yT_scale.shape[0]), _p(dev_status), _stream())
+    return yT, yT_scale
+
+
+def fp8_matmul_wgrad_workspace(M: int, N: int, K: int, G: int) -> int:
+    """Bytes of workspace fp8_matmul_wgrad needs (-1 for a rejected shape)."""
+    return int(abi().fp8_matmul_wgrad_workspace(int(M), int(N), int(K), int(G)))
+
+
+def fp8_matmul_wgrad(aT: torch.Tensor, aT_scale: torch.Tensor, bT: torch.Tensor,
+                     bT_scale: torch.Tensor, group_offsets: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
+                     accumulate: bool = False, workspace: torch.Tensor | None = None,
+                     dev_status: torch.Tensor | None = None):
+    """Per group the product over its tokens of aT (uint8 [N, M], scales [cap,
+    N]) and bT (uint8 [K, M], scales [cap, K]), both as fp8_quantize_cols or
+    fp4_to_fp8_cols give them -> out [G, N, K] (float32 or BF16), added to what
+    `out` holds if `accumulate`."""
+    _need(aT, torch.uint8, "aT", 2)
+    _need(bT, torch.uint8, "bT", 2)
+    N, M = aT.shape
+    K = bT.shape[0]
+    if bT.shape[1] != M:
+        raise ValueError(f"bT must have {M} tokens like aT, got {bT.shape[1]}")
+    G = 1 if group_offsets is None else _groups(group_offsets)
+    cap = fp4_to_fp8_cols_scale_capacity(M, G)
+    for t, name, rows in ((aT_scale, "aT_scale", N), (bT_scale, "bT_scale", K)):
+        _need(t, torch.float32, name, 2)
+        if t.shape[1] != rows or t.shape[0] < cap:
+            raise ValueError(f"{name} must be [>= {cap}, {rows}], got {tuple(t.shape)}")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    dt = _out_dtype(out, out_dtype)
+    out = _empty((G, N, K), dt, aT) if out is None else out
+    _need(out, dt, "out", numel=G * N * K)
+    need = fp8_matmul_wgrad_workspace(M, N, K, G)
+    workspace = _empty((max(need, 0),), torch.uint8, aT) if workspace is None else workspace
+    _need(workspace, torch.uint8, "workspace")
+    if workspace.numel() < need:
+        raise ValueError(f"workspace must hold {need} bytes, got {workspace.numel()}")
+    _dev_status(dev_status)
+    _on_device(aT=aT, aT_scale=aT_scale, bT=bT, bT_scale=bT_scale, group_offsets=group_offsets,
+               out=out, workspace=workspace, dev_status=dev_status)
+    _call("fp8_matmul_wgrad", _p(aT), _p(aT_scale), N, _p(bT), _p(bT_scale), K, M,
+          _p(group_offsets), G, min(aT_scale.shape[0], bT_scale.shape[0]), _p(out),
+          int(dt == torch.float32), int(bool(accumulate)), _p(workspace), workspace.numel(),
+          _p(dev_status), _stream())
+    return out
+
+
+# ---------------------------------------------------------------- routing to experts
+
+def _logits(logits, score):
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError(f'score must be "softmax" or "sigmoid", got {score!r}')
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits must be a float32 or bfloat16 tensor")
+    _need(logits, logits.dtype, "logits", 2)
+    return logits.shape
+
+
+def moe_route(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None,
+              score: str = "softmax", n_groups: int = 1, keep_groups: int = 1, group_top: int = 1,
+              renormalize: bool = True, scale: float = 1.0, weights: torch.Tensor | None = None,
+              ids: torch.Tensor | None = None):
+    """Router logits [T, E] (float32 or BF16) -> (weights float32 [T, k], ids
+    int32 [T, k]): softmax or sigmoid scores, `bias` float32 [E] added for the
+    choice only, the choice limited to the `keep_groups` best of `n_groups`
+    runs of experts, weights divided by their sum if `renormalize`, times
+    `scale`.  A slot without an available expert has id -1 and weight 0."""
+    T, E = _logits(logits, score)
+    weights = _empty((T, k), torch.float32, logits) if weights is None else weights
+    ids = _empty((T, k), torch.int32, logits) if ids is None else ids
+    _need(weights, torch.float32, "weights", numel=T * k)
+    _need(ids, torch.int32, "ids", numel=T * k)
+    if bias is not None:
+        _need(bias, torch.float32, "bias", numel=E)
+    _on_device(logits=logits, bias=bias, weights=weights, ids=ids)
+    _call("moe_route", _p(logits), int(logits.dtype == torch.float32), T, E, int(k), _p(bias),
+          int(score == "sigmoid"), int(n_groups), int(keep_groups), int(group_top),
+          int(bool(renormalize)), float(scale), _p(weights), _p(ids), _stream())
+    return weights, ids
+
+
+def moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor,
+                       score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                       dlogits: torch.Tensor | None = None):
+    """Gradient of moe_route's weights for its ids: dweights float32 [T, k] ->
+    dlogits [T, E] in the logits' type."""
+    T, E = _logits(logits, score)
+    _need(ids, torch.int32, "ids", 2)
+    k = ids.shape[1]
+    _need(ids, torch.int32, "ids", shape=(T, k))
+    _need(dweights, torch.float32, "dweights", shape=(T, k))
+    dlogits = _empty((T, E), logits.dtype, logits) if dlogits is None else dlogits
+    _need(dlogits, logits.dtype, "dlogits", numel=T * E)
+    _on_device(logits=logits, ids=ids, dweights=dweights, dlogits=dlogits)
+    _call("moe_route_backward", _p(logits), int(logits.dtype == torch.float32), T, E, _p(ids),
+          _p(dweights), k, int(score == "sigmoid"), int(bool(renormalize)), float(scale),
+          _p(dlogits), _stream())
+    return dlogits
+
+
+def moe_sort_rows(ids: torch.Tensor, n_experts: int, group_offsets: torch.Tensor | None = None,
+                  pair_of_row: torch.Tensor | None = None,
+                  row_of_pair: torch.Tensor | None = None):
+    """Expert ids int32 (any shape, e.g. [T, k]) -> (group_offsets int64 [E+1],
+    pair_of_row int32 [n], row_of_pair int32 shaped like ids): the (token,
+    choice) pairs ordered by expert, and within an expert by index.  Row r
+    holds token pair_of_row[r] // k; ids outside [0, E) get no row (-1)."""
+    _need(ids, torch.int32, "ids")
+    n, E = ids.numel(), int(n_experts)
+    group_offsets = _empty((max(E, 0) + 1,), torch.int64, ids) if group_offsets is None else group_offsets
+    pair_of_row = _empty((n,), torch.int32, ids) if pair_of_row is None else pair_of_row
+    row_of_pair = torch.empty_like(ids) if row_of_pair is None else row_of_pair
+    _need(group_offsets, torch.int64, "group_offsets", numel=E + 1 if E > 0 else None)
+    _need(pair_of_row, torch.int32, "pair_of_row", numel=n)
+    _need(row_of_pair, torch.int32, "row_of_pair", numel=n)
+    _on_device(ids=ids, group_offsets=group_offsets, pair_of_row=pair_of_row,
+               row_of_pair=row_of_pair)
+    _call("moe_sort_rows", _p(ids), n, E, _p(group_offsets), _p(pair_of_row), _p(row_of_pair),
+          _stream())
+    return group_offsets, pair_of_row, row_of_pair
 
 
 def mxfp4_dequantize_rows(q: torch.Tensor, s: torch.Tensor, out: torch.Tensor | None = None):

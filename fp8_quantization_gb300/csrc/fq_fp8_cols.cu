@@ -1,0 +1,191 @@
+// BF16 -> transposed FP8 E4M3 on ragged token groups: the weight gradient's
+// operand, quantized along the tokens.
+//
+// Source: "Practical FP4 Training for Large-Scale MoE Models on Hopper GPUs",
+// technical overview section 2: gradients stay in standard FP8 (item 2); the
+// transposed operand's 128-token blocks follow the ragged per-expert groups
+// without padding (item 3).  Quantizer, per block of at most 128 tokens of one
+// group and one feature (binary32, one rounding per operation):
+//   r = min(448 / amax, FLT_MAX), s = amax / 448, code = E4M3(x * r);
+//   a block holding NaN or Inf gets s = NaN and codes 0x7F.
+//
+// Bound by HBM: 2 bytes read and 1 written per element, 4 bytes written per
+// block and feature.
+#include <cfloat>
+
+#include "fq_tc.cuh"
+
+namespace fq {
+
+namespace {
+
+constexpr int kTok = 128;   // tokens of a block
+constexpr int kFeat = 128;  // features of a tile
+
+// Byte of (feature, token) of a tile in shared memory: rows of 128 tokens,
+// 8 bytes further after every 8 features.  A half-warp storing 8 tokens of 16
+// features 8 apart then touches 16 different 8-byte bank pairs.
+__device__ __forceinline__ int tile_byte(int f, int t) { return f * kTok + (f >> 3) * 8 + t; }
+constexpr int kTileBytes = kFeat * kTok + (kFeat / 8) * 8 + 16;
+
+__device__ __forceinline__ uint32_t cvt_e4m3_pair(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// One CTA tile = one 128-token block x 128 features.  Thread (q, c), q = 0..15
+// and c = 0..15, holds tokens 8q..8q+7 of features 8c..8c+7: 16-byte loads of
+// 256-byte row segments, the block maxima over the q by shuffle and shared
+// memory, and 8 codes of one feature as one 8-byte shared store (the
+// conversion takes two tokens of a feature at a time, so nothing is
+// transposed in registers).  Rows of the transposed tile start at any byte of
+// yT: they are written as aligned 4-byte words, the bytes at both ends alone.
+__global__ void __launch_bounds__(kThreads) fp8_quantize_cols_kernel(
+    const uint16_t *__restrict__ x, int32_t M, int32_t K, const int64_t *__restrict__ offs,
+    int32_t G, uint8_t *__restrict__ yT, float *__restrict__ scale, int64_t cap, int32_t *dev_status)
+{
+    extern __shared__ int32_t dyn[];
+    __shared__ uint32_t red[kThreads / 32][kFeat / 2];
+    __shared__ __align__(16) uint8_t tile[kTileBytes];
+    int32_t *off = dyn, *first = dyn + G + 2;
+    const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+    const int q = tid >> 4, c = tid & 15;
+
+    griddep_wait();  // the previous kernel's outputs (PDL launch)
+    if (wid == 0) {
+        const bool bad = load_row_groups(offs, G, M, kTok, off, first);
+        if (bad && dev_status && blockIdx.x == 0 && lane == 0)
+            atomicOr(dev_status, 1);
+    }
+    __syncthreads();
+    const int32_t blocks = first[G + 1], used = first[G];
+    const int32_t slabs = (K + kFeat - 1) / kFeat;
+    // scale rows past the last block are 0
+    for (int64_t i = static_cast<int64_t>(used) * K + blockIdx.x * kThreads + tid; i < cap * K;
+         i += static_cast<int64_t>(gridDim.x) * kThreads)
+        scale[i] = 0.0f;
+
+    const int64_t tiles = static_cast<int64_t>(blocks) * slabs;
+    for (int64_t idx = blockIdx.x; idx < tiles; idx += gridDim.x) {
+        const int32_t slab = static_cast<int32_t>(idx / blocks);
+        const int32_t blk = static_cast<int32_t>(idx - static_cast<int64_t>(slab) * blocks);
+        const int g = group_of_tile(first, G + 1, blk);
+        const int32_t t0 = off[g] + (blk - first[g]) * kTok;
+        const int32_t len = min(kTok, off[g + 1] - t0);
+        const int32_t f0 = slab * kFeat, f = f0 + 8 * c;
+
+        uint4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int t = 8 * q + j;
+            v[j] = g < G && t < len && f < K
+                       ? ld_nc_v4(x + static_cast<int64_t>(t0 + t) * K + f)
+                       : make_uint4(0, 0, 0, 0);
+        }
+        uint32_t m[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            m[0] = absmax_bf16x2(m[0], v[j].x);
+            m[1] = absmax_bf16x2(m[1], v[j].y);
+            m[2] = absmax_bf16x2(m[2], v[j].z);
+            m[3] = absmax_bf16x2(m[3], v[j].w);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            m[i] = max_u16x2(m[i], __shfl_xor_sync(0xffffffffu, m[i], 16));
+        if (lane < 16)
+            *reinterpret_cast<uint4 *>(&red[wid][4 * c]) = make_uint4(m[0], m[1], m[2], m[3]);
+        __syncthreads();  // also: the previous tile's rows are written out
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; w++) {
+            const uint4 o = *reinterpret_cast<const uint4 *>(&red[w][4 * c]);
+            m[0] = max_u16x2(m[0], o.x);
+            m[1] = max_u16x2(m[1], o.y);
+            m[2] = max_u16x2(m[2], o.z);
+            m[3] = max_u16x2(m[3], o.w);
+        }
+        const uint32_t *vw = reinterpret_cast<const uint32_t *>(v);
+        float sc[8];
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const uint32_t bits = (e & 1) ? m[e >> 1] >> 16 : m[e >> 1] & 0xFFFFu;
+            const float amax = __uint_as_float(bits << 16);
+            const bool special = bits >= 0x7F80u;
+            const float r = fminf(__fdiv_rn(448.0f, amax), FLT_MAX);
+            sc[e] = special ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, 448.0f);
+            uint32_t w[2];
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                float p[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const uint32_t u = vw[4 * (4 * h + j) + (e >> 1)];
+                    p[j] = (e & 1) ? bf16_hi(u) : bf16_lo(u);
+                }
+                fmul2(p[0], p[1], r, p[0], p[1]);
+                fmul2(p[2], p[3], r, p[2], p[3]);
+                w[h] = cvt_e4m3_pair(p[0], p[1]) | (cvt_e4m3_pair(p[2], p[3]) << 16);
+                if (special)
+                    w[h] = 0x7F7F7F7Fu;
+            }
+            *reinterpret_cast<uint2 *>(tile + tile_byte(8 * c + e, 8 * q)) = make_uint2(w[0], w[1]);
+        }
+        if (q == 0 && g < G && f < K) {
+            float4 *d = reinterpret_cast<float4 *>(scale + static_cast<int64_t>(blk) * K + f);
+            d[0] = make_float4(sc[0], sc[1], sc[2], sc[3]);
+            d[1] = make_float4(sc[4], sc[5], sc[6], sc[7]);
+        }
+        __syncthreads();
+        // row f0 + r of yT: bytes t0 .. t0 + len - 1, a warp per row
+        for (int r = wid; r < kFeat && f0 + r < K; r += kThreads / 32) {
+            uint8_t *dst = yT + static_cast<int64_t>(f0 + r) * M + t0;
+            const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(dst) & 3u);
+            const uint8_t *src = tile + tile_byte(r, 0);
+            for (int i = 4 * lane - mis; i < len; i += 128) {  // word at token i
+                if (i >= 0 && i + 4 <= len) {
+                    const uint32_t *s4 = reinterpret_cast<const uint32_t *>(src + (i & ~3));
+                    const uint32_t w = (i & 3) ? __funnelshift_r(s4[0], s4[1], 8 * (i & 3)) : s4[0];
+                    *reinterpret_cast<uint32_t *>(dst + i) = w;
+                } else {
+                    for (int b = max(i, 0); b < min(i + 4, len); b++)
+                        dst[b] = src[b];
+                }
+            }
+        }
+    }
+}
+
+}  // namespace
+
+}  // namespace fq
+
+extern "C" fq_status fp8_quantize_cols(const void *x, int64_t M, int64_t K,
+                                       const int64_t *group_offsets, int32_t G, uint8_t *yT,
+                                       float *yT_scale, int64_t cap, int32_t *dev_status,
+                                       void *stream)
+{
+    using namespace fq;
+    if (M < 0 || M > INT32_MAX - 512 || K <= 0 || K % 8 != 0 || K > INT32_MAX - 512)
+        return FQ_ERR_SHAPE;
+    if (G < 1 || G > FQ_COLS_MAX_GROUPS || (!group_offsets && G != 1))
+        return FQ_ERR_ARG;
+    if (cap < fp4_to_fp8_cols_scale_capacity(M, G))
+        return FQ_ERR_ARG;
+    if (cap > INT64_MAX / 4 / K)
+        return FQ_ERR_SHAPE;
+    if ((M > 0 && (!x || !yT)) || !yT_scale)
+        return FQ_ERR_NULL;
+    if (!aligned16(x) || !aligned16(group_offsets) || !aligned16(yT) || !aligned16(yT_scale))
+        return FQ_ERR_ALIGN;
+    const size_t dyn = 2 * (G + 2) * sizeof(int32_t);
+    const int64_t tiles = fp4_to_fp8_cols_scale_capacity(M, G) * ((K + kFeat - 1) / kFeat);
+    const int grid = persistent_grid(fp8_quantize_cols_kernel, kThreads, dyn, tiles);
+    if (launch_pdl(fp8_quantize_cols_kernel, dim3(grid), dim3(kThreads), dyn,
+                   static_cast<cudaStream_t>(stream), static_cast<const uint16_t *>(x),
+                   static_cast<int32_t>(M), static_cast<int32_t>(K), group_offsets, G, yT, yT_scale,
+                   cap, dev_status) != cudaSuccess)
+        return launch_status();
+    return launch_status();
+}

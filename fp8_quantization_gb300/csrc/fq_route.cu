@@ -1,0 +1,585 @@
+// Routing of tokens to experts: scores, choice, weights, their gradient, and
+// the order of the rows that the ragged per-expert calls take.
+//
+// Source: "Practical FP4 Training for Large-Scale MoE Models on Hopper GPUs",
+// technical overview section 2 item 3: tokens form ragged per-expert groups
+// without padding.  The pages fix no router; the forms are the usual ones:
+//   score  s_e = exp(l_e) / sum_f exp(l_f)   or   1 / (1 + exp(-l_e))
+//   choice c_e = s_e + bias_e (the bias balances the experts and takes no part
+//          in the weights); with expert groups only the experts of the
+//          `keep` groups with the largest sum of their best `top` choices
+//   ids    the k largest choices, ties to the lowest index
+//   weight w_j = scale * s_j, or scale * s_j / (sum of the chosen s)
+// in binary32.  A logit that is NaN or at or below BF16's lowest finite value
+// masks its expert: never chosen, score 0.  A slot without an expert (fewer
+// than k available) gets id -1 and weight 0.
+#include <cfloat>
+#include <cmath>
+
+#include "fq_common.cuh"
+
+namespace fq {
+
+namespace {
+
+constexpr float kMasked = -0x1.FEp127f;  // BF16's lowest finite value
+constexpr int kWarps = kThreads / 32;
+constexpr unsigned kFull = 0xffffffffu;
+
+struct RouteArgs {
+    const void *logits;
+    const float *bias;
+    int64_t T;
+    int32_t E, k;
+    int32_t n_groups, keep, top;
+    float scale;
+    float *w;
+    int32_t *ids;
+};
+
+template <bool kBf16>
+__device__ __forceinline__ float load_logit(const void *logits, int64_t at)
+{
+    return kBf16 ? bf16_lo(__ldg(static_cast<const uint16_t *>(logits) + at))
+                 : __ldg(static_cast<const float *>(logits) + at);
+}
+
+__device__ __forceinline__ float sigmoid_score(float l) { return __fdiv_rn(1.0f, 1.0f + expf(-l)); }
+
+// Unsigned key in the order of the floats (never 0 for a number above -inf).
+__device__ __forceinline__ uint32_t order_key(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k)
+{
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        v += __shfl_xor_sync(kFull, v, d);
+    return v;
+}
+
+// Largest key of the warp and the lowest index that has it; 0 if none.
+__device__ __forceinline__ uint32_t warp_best(uint32_t key, int idx, int &best)
+{
+    const uint32_t m = __reduce_max_sync(kFull, key);
+    best = static_cast<int>(__reduce_min_sync(kFull, key == m ? static_cast<unsigned>(idx) : 0x7fffffffu));
+    return m;
+}
+
+// One warp per token; lane l holds the experts l + 32 i.  kVals >= E / 32.
+template <int kVals, bool kBf16, bool kSigmoid, bool kNorm>
+__global__ void __launch_bounds__(kThreads) moe_route_kernel(const RouteArgs p)
+{
+    griddep_wait();  // the previous kernel's outputs (PDL launch)
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int per_group = p.E / p.n_groups;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < p.T;
+         t += static_cast<int64_t>(gridDim.x) * kWarps) {
+        const int64_t row = t * p.E;
+        float l[kVals];
+        float mx = -FLT_MAX;
+#pragma unroll
+        for (int i = 0; i < kVals; i++) {
+            const int e = lane + 32 * i;
+            l[i] = e < p.E ? load_logit<kBf16>(p.logits, row + e) : -INFINITY;
+            if (l[i] > kMasked)
+                mx = fmaxf(mx, fminf(l[i], FLT_MAX));
+        }
+        float sum = 1.0f;
+        if (!kSigmoid) {
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
+            sum = 0.0f;
+        }
+        uint32_t key[kVals];
+#pragma unroll
+        for (int i = 0; i < kVals; i++) {
+            const bool ok = l[i] > kMasked;
+            float s = 0.0f;
+            if (ok)
+                s = kSigmoid ? sigmoid_score(fminf(l[i], FLT_MAX)) : expf(fminf(l[i], FLT_MAX) - mx);
+            if (!kSigmoid)
+                sum += s;
+            l[i] = s;
+            key[i] = ok;
+        }
+        if (!kSigmoid)
+            sum = warp_sum(sum);
+#pragma unroll
+        for (int i = 0; i < kVals; i++) {
+            float c = l[i];
+            const int e = lane + 32 * i;
+            if (p.bias && e < p.E)
+                c = (kSigmoid ? c : __fdiv_rn(c, sum)) + __ldg(p.bias + e);
+            key[i] = key[i] && c > -INFINITY ? order_key(c) : 0u;
+        }
+
+        if (p.n_groups > 1) {
+            // score of group g in lane g
+            uint32_t score = 0;
+            for (int g = 0; g < p.n_groups; g++) {
+                const int lo = g * per_group, hi = lo + per_group;
+                uint32_t m = 0;
+                int at = 0;
+#pragma unroll
+                for (int i = 0; i < kVals; i++) {
+                    const int e = lane + 32 * i;
+                    if (e >= lo && e < hi && key[i] > m) {
+                        m = key[i];
+                        at = e;
+                    }
+                }
+                int b1;
+                const uint32_t k1 = warp_best(m, at, b1);
+                uint32_t sk = k1;
+                if (p.top == 2) {
+                    m = 0;
+#pragma unroll
+                    for (int i = 0; i < kVals; i++) {
+                        const int e = lane + 32 * i;
+                        if (e >= lo && e < hi && e != b1 && key[i] > m)
+                            m = key[i];
+                    }
+                    const uint32_t k2 = __reduce_max_sync(kFull, m);
+                    if (k2) {
+                        const float v = key_value(k1) + key_value(k2);
+                        sk = order_key(v == 0.0f ? 0.0f : v);
+                    }
+                }
+                if (lane == g)
+                    score = sk;
+            }
+            uint32_t kept = 0;
+            for (int j = 0; j < p.keep; j++) {
+                int g;
+                if (!warp_best(score, lane, g))
+                    break;
+                kept |= 1u << g;
+                if (lane == g)
+                    score = 0;
+            }
+#pragma unroll
+            for (int i = 0; i < kVals; i++) {
+                const int e = lane + 32 * i;
+                if (e < p.E && !((kept >> (e / per_group)) & 1u))
+                    key[i] = 0;
+            }
+        }
+
+        int id = -1;  // of slot `lane`
+        for (int j = 0; j < p.k; j++) {
+            uint32_t m = 0;
+            int at = 0;
+#pragma unroll
+            for (int i = 0; i < kVals; i++)
+                if (key[i] > m) {
+                    m = key[i];
+                    at = lane + 32 * i;
+                }
+            int e;
+            if (!warp_best(m, at, e))
+                break;
+            if (lane == j)
+                id = e;
+#pragma unroll
+            for (int i = 0; i < kVals; i++)
+                if (lane + 32 * i == e)
+                    key[i] = 0;
+        }
+        float w = 0.0f;
+        if (id >= 0) {
+            const float v = fminf(load_logit<kBf16>(p.logits, row + id), FLT_MAX);
+            w = kSigmoid ? sigmoid_score(v) : expf(v - mx);
+        }
+        if (kNorm)
+            sum = warp_sum(w);
+        if (kNorm || !kSigmoid)
+            w = sum > 0.0f ? __fdiv_rn(w, sum) : 0.0f;
+        if (lane < p.k) {
+            p.w[t * p.k + lane] = w * p.scale;
+            p.ids[t * p.k + lane] = id;
+        }
+    }
+}
+
+struct RouteGradArgs {
+    const void *logits;
+    const int32_t *ids;
+    const float *dw;
+    int64_t T;
+    int32_t E, k;
+    float scale;
+    void *dl;
+};
+
+__device__ __forceinline__ void store_grad(void *dl, int64_t at, float v, bool bf16)
+{
+    if (bf16)
+        static_cast<uint16_t *>(dl)[at] = static_cast<uint16_t>([&] {
+            uint32_t r;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.0f), "f"(v));
+            return r;
+        }());
+    else
+        static_cast<float *>(dl)[at] = v;
+}
+
+// One warp per token.  With q_j = s_j / sum of the chosen s (normalised) the
+// gradient of a chosen score is ds_j = scale (dw_j - sum_i dw_i q_i) / sum;
+// through the softmax that is dl_j = scale q_j (dw_j - sum_i dw_i q_i) and 0
+// elsewhere, which needs the chosen logits only.  Not normalised, softmax:
+// dl_e = p_e (ds_e - sum_j ds_j p_j) for every expert.
+template <bool kBf16, bool kSigmoid, bool kNorm>
+__global__ void __launch_bounds__(kThreads) moe_route_backward_kernel(const RouteGradArgs p)
+{
+    griddep_wait();  // the previous kernel's outputs (PDL launch)
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < p.T;
+         t += static_cast<int64_t>(gridDim.x) * kWarps) {
+        const int64_t row = t * p.E;
+        int id = lane < p.k ? __ldg(p.ids + t * p.k + lane) : -1;
+        float l = -INFINITY, dw = 0.0f;
+        if (id >= 0 && id < p.E)
+            l = load_logit<kBf16>(p.logits, row + id);
+        if (l > kMasked) {
+            l = fminf(l, FLT_MAX);
+            dw = __ldg(p.dw + t * p.k + lane) * p.scale;
+        } else {
+            id = -1;
+        }
+        float d = 0.0f, rest = 0.0f;  // gradient of the slot's logit; of another logit: -rest * p_e
+        float mx = -FLT_MAX, inv = 0.0f;
+        if (kSigmoid) {
+            const float s = id >= 0 ? sigmoid_score(l) : 0.0f;
+            float ds = dw;
+            if (kNorm) {
+                const float sum = warp_sum(s);
+                const float mean = sum > 0.0f ? __fdiv_rn(warp_sum(dw * s), sum) : 0.0f;
+                ds = sum > 0.0f ? __fdiv_rn(dw - mean, sum) : 0.0f;
+            }
+            d = ds * s * (1.0f - s);
+        } else {
+            if (id >= 0)
+                mx = l;
+            if (!kNorm)
+                for (int e = lane; e < p.E; e += 32) {
+                    const float v = load_logit<kBf16>(p.logits, row + e);
+                    if (v > kMasked)
+                        mx = fmaxf(mx, fminf(v, FLT_MAX));
+                }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+            const float ex = id >= 0 ? expf(l - mx) : 0.0f;
+            float sum = ex;
+            if (!kNorm) {
+                sum = 0.0f;
+                for (int e = lane; e < p.E; e += 32) {
+                    const float v = load_logit<kBf16>(p.logits, row + e);
+                    if (v > kMasked)
+                        sum += expf(fminf(v, FLT_MAX) - mx);
+                }
+            }
+            sum = warp_sum(sum);
+            inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+            const float q = ex * inv;
+            rest = warp_sum(dw * q);
+            d = q * (dw - rest);
+        }
+        for (int e = lane; e < p.E; e += 32) {
+            float v = 0.0f;
+            if (!kSigmoid && !kNorm) {
+                const float x = load_logit<kBf16>(p.logits, row + e);
+                if (x > kMasked)
+                    v = -rest * (expf(fminf(x, FLT_MAX) - mx) * inv);
+            }
+            store_grad(p.dl, row + e, v, kBf16);
+        }
+        __syncwarp();  // the chosen logits' gradients go over the row
+        if (id >= 0)
+            store_grad(p.dl, row + id, d, kBf16);
+    }
+}
+
+// ---------------------------------------------------------------- rows by expert
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// A 32-bit word of another CTA's shared memory, by the address of one's own.
+__device__ __forceinline__ uint32_t ld_cluster(const uint32_t *own, uint32_t rank)
+{
+    uint32_t a, v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(own)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortCluster = 8;
+
+// Stable counting sort by one cluster.  Every warp owns a run of consecutive
+// pairs: it counts its pairs per expert in its own counters, the counters
+// become start rows (over the experts, then the CTAs, then the warps), and
+// the warp goes over its run again in order, a pair's row being its expert's
+// counter plus its rank among the lanes with the same expert.
+__global__ void __launch_bounds__(kSortThreads) moe_sort_rows_kernel(
+    const int32_t *__restrict__ ids, int64_t n, int32_t E, int64_t *__restrict__ offs,
+    int32_t *__restrict__ pair_of_row, int32_t *__restrict__ row_of_pair)
+{
+    extern __shared__ uint32_t smem[];
+    __shared__ uint32_t warp_tot[kSortWarps];
+    uint32_t *total = smem, *count = smem + E;  // [E], [kSortWarps][E]
+    const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank(), ctas = cluster_size();
+    for (int i = tid; i < kSortWarps * E; i += kSortThreads)
+        count[i] = 0;
+    __syncthreads();
+    griddep_wait();  // the previous kernel's outputs (PDL launch)
+    griddep_launch_dependents();
+
+    uint32_t *mine = count + wid * E;
+    const int64_t per = ((n + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
+    const int64_t lo = min(n, per * (rank * kSortWarps + wid)), hi = min(n, lo + per);
+    for (int64_t i = lo + lane; i < hi; i += 32) {
+        const int32_t e = __ldg(ids + i);
+        if (e >= 0 && e < E)
+            atomicAdd(mine + e, 1u);
+    }
+    __syncthreads();
+    if (tid < E) {
+        uint32_t run = 0;
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; w++) {
+            const uint32_t c = count[w * E + tid];
+            count[w * E + tid] = run;
+            run += c;
+        }
+        total[tid] = run;
+    }
+    cluster_arrive();
+    cluster_wait();
+    uint32_t before = 0, all = 0;  // pairs of expert tid: in the CTAs before this one, in all
+    if (tid < E)
+        for (uint32_t r = 0; r < ctas; r++) {
+            const uint32_t v = ld_cluster(total + tid, r);
+            before += r < rank ? v : 0;
+            all += v;
+        }
+    cluster_arrive();  // the last read of another CTA's memory
+    uint32_t incl = all;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t u = __shfl_up_sync(kFull, incl, d);
+        if (lane >= d)
+            incl += u;
+    }
+    if (lane == 31)
+        warp_tot[wid] = incl;
+    __syncthreads();
+    uint32_t start = incl - all, rows = 0;
+    for (int w = 0; w < kSortWarps; w++) {
+        const uint32_t v = warp_tot[w];
+        start += w < wid ? v : 0;
+        rows += v;
+    }
+    if (tid < E) {
+        if (rank == 0) {
+            offs[tid] = start;
+            if (tid == E - 1)
+                offs[E] = rows;
+        }
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; w++)
+            count[w * E + tid] += start + before;
+    }
+    __syncthreads();
+    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+        const int64_t i = i0 + lane;
+        int32_t e = i < hi ? __ldg(ids + i) : -1;
+        if (e < 0 || e >= E)
+            e = -1;
+        const unsigned same = __match_any_sync(kFull, e);
+        int32_t row = -1;
+        if (e >= 0)
+            row = static_cast<int32_t>(mine[e] + __popc(same & ((1u << lane) - 1)));
+        __syncwarp();
+        if (e >= 0 && lane == __ffs(same) - 1)
+            mine[e] += __popc(same);
+        __syncwarp();
+        if (i < hi) {
+            row_of_pair[i] = row;
+            if (row >= 0)
+                pair_of_row[row] = static_cast<int32_t>(i);
+        }
+    }
+    // rows of no expert
+    for (int64_t r = rows + static_cast<int64_t>(rank) * kSortThreads + tid; r < n;
+         r += static_cast<int64_t>(ctas) * kSortThreads)
+        pair_of_row[r] = -1;
+    cluster_wait();
+}
+
+template <int kVals>
+void *route_kernel(bool bf16, bool sigmoid, bool norm)
+{
+#define FQ_PICK(B, S, N) reinterpret_cast<void *>(moe_route_kernel<kVals, B, S, N>)
+    if (bf16)
+        return sigmoid ? (norm ? FQ_PICK(true, true, true) : FQ_PICK(true, true, false))
+                       : (norm ? FQ_PICK(true, false, true) : FQ_PICK(true, false, false));
+    return sigmoid ? (norm ? FQ_PICK(false, true, true) : FQ_PICK(false, true, false))
+                   : (norm ? FQ_PICK(false, false, true) : FQ_PICK(false, false, false));
+#undef FQ_PICK
+}
+
+using RouteKernel = void (*)(const RouteArgs);
+using RouteGradKernel = void (*)(const RouteGradArgs);
+
+RouteGradKernel grad_kernel(bool bf16, bool sigmoid, bool norm)
+{
+#define FQ_PICK(B, S, N) moe_route_backward_kernel<B, S, N>
+    if (bf16)
+        return sigmoid ? (norm ? FQ_PICK(true, true, true) : FQ_PICK(true, true, false))
+                       : (norm ? FQ_PICK(true, false, true) : FQ_PICK(true, false, false));
+    return sigmoid ? (norm ? FQ_PICK(false, true, true) : FQ_PICK(false, true, false))
+                   : (norm ? FQ_PICK(false, false, true) : FQ_PICK(false, false, false));
+#undef FQ_PICK
+}
+
+bool flag(int v) { return v == 0 || v == 1; }
+
+}  // namespace
+
+}  // namespace fq
+
+extern "C" fq_status moe_route(const void *logits, int logits_f32, int64_t T, int32_t E, int32_t k,
+                               const float *bias, int sigmoid, int32_t n_groups,
+                               int32_t keep_groups, int32_t group_top, int renormalize, float scale,
+                               float *weights, int32_t *ids, void *stream)
+{
+    using namespace fq;
+    if (T < 0 || T > INT64_MAX / 4096)
+        return FQ_ERR_SHAPE;
+    if (E < 1 || E > FQ_COLS_MAX_GROUPS || k < 1 || k > FQ_ROUTE_MAX_K || k > E ||
+        !flag(logits_f32) || !flag(sigmoid) || !flag(renormalize) || n_groups < 1 ||
+        n_groups > FQ_ROUTE_MAX_GROUPS || E % n_groups != 0 || keep_groups < 1 ||
+        keep_groups > n_groups || group_top < 1 || group_top > 2)
+        return FQ_ERR_ARG;
+    if (T == 0)
+        return FQ_OK;
+    if (!logits || !weights || !ids)
+        return FQ_ERR_NULL;
+    if (!aligned16(logits) || !aligned16(bias) || !aligned16(weights) || !aligned16(ids))
+        return FQ_ERR_ALIGN;
+    const RouteArgs p = {logits, bias, T, E, k, n_groups, keep_groups, group_top, scale, weights,
+                         ids};
+    const bool bf16 = !logits_f32;
+    const int vals = (E + 31) / 32;
+    void *kern = vals <= 1   ? route_kernel<1>(bf16, sigmoid, renormalize)
+                 : vals <= 2 ? route_kernel<2>(bf16, sigmoid, renormalize)
+                 : vals <= 4 ? route_kernel<4>(bf16, sigmoid, renormalize)
+                 : vals <= 8 ? route_kernel<8>(bf16, sigmoid, renormalize)
+                 : vals <= 16 ? route_kernel<16>(bf16, sigmoid, renormalize)
+                              : route_kernel<32>(bf16, sigmoid, renormalize);
+    const RouteKernel f = reinterpret_cast<RouteKernel>(kern);
+    const int grid = persistent_grid(f, kThreads, 0, (T + kWarps - 1) / kWarps, 4);
+    if (launch_pdl(f, dim3(grid), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), p) !=
+        cudaSuccess)
+        return launch_status();
+    return launch_status();
+}
+
+extern "C" fq_status moe_route_backward(const void *logits, int logits_f32, int64_t T, int32_t E,
+                                        const int32_t *ids, const float *dweights, int32_t k,
+                                        int sigmoid, int renormalize, float scale, void *dlogits,
+                                        void *stream)
+{
+    using namespace fq;
+    if (T < 0 || T > INT64_MAX / 4096)
+        return FQ_ERR_SHAPE;
+    if (E < 1 || E > FQ_COLS_MAX_GROUPS || k < 1 || k > FQ_ROUTE_MAX_K || k > E ||
+        !flag(logits_f32) || !flag(sigmoid) || !flag(renormalize))
+        return FQ_ERR_ARG;
+    if (T == 0)
+        return FQ_OK;
+    if (!logits || !ids || !dweights || !dlogits)
+        return FQ_ERR_NULL;
+    if (!aligned16(logits) || !aligned16(ids) || !aligned16(dweights) || !aligned16(dlogits))
+        return FQ_ERR_ALIGN;
+    const RouteGradArgs p = {logits, ids, dweights, T, E, k, scale, dlogits};
+    const RouteGradKernel f = grad_kernel(!logits_f32, sigmoid, renormalize);
+    const int grid = persistent_grid(f, kThreads, 0, (T + kWarps - 1) / kWarps, 4);
+    if (launch_pdl(f, dim3(grid), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), p) !=
+        cudaSuccess)
+        return launch_status();
+    return launch_status();
+}
+
+extern "C" fq_status moe_sort_rows(const int32_t *ids, int64_t n, int32_t E, int64_t *group_offsets,
+                                   int32_t *pair_of_row, int32_t *row_of_pair, void *stream)
+{
+    using namespace fq;
+    if (n < 0 || n > INT32_MAX - 512)
+        return FQ_ERR_SHAPE;
+    if (E < 1 || E > FQ_COLS_MAX_GROUPS)
+        return FQ_ERR_ARG;
+    if (!group_offsets || (n > 0 && (!ids || !pair_of_row || !row_of_pair)))
+        return FQ_ERR_NULL;
+    if (!aligned16(ids) || !aligned16(group_offsets) || !aligned16(pair_of_row) ||
+        !aligned16(row_of_pair))
+        return FQ_ERR_ALIGN;
+    const size_t dyn = (kSortWarps + 1) * static_cast<size_t>(E) * sizeof(uint32_t);
+    if (cudaFuncSetAttribute(moe_sort_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(dyn)) != cudaSuccess)
+        return launch_status();
+    // one CTA up to 4 pairs a thread
+    unsigned ctas = 1;
+    while (ctas < kSortCluster && n > static_cast<int64_t>(ctas) * 4 * kSortThreads)
+        ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = dyn;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, moe_sort_rows_kernel, ids, n, E, group_offsets, pair_of_row,
+                           row_of_pair) != cudaSuccess)
+        return launch_status();
+    return launch_status();
+}

@@ -249,6 +249,107 @@ fq_status fp8_matmul(const uint8_t *a, const float *sa, int64_t M, int64_t K, co
                      int32_t G, void *c, int c_f32, int32_t *dev_status, void *stream);
 
 /*
+ * BF16 -> transposed FP8 E4M3 on ragged token groups ([MoE-FP4] 2.2: gradients
+ * stay in standard FP8; 2.3: the transposed operand's blocks follow the
+ * ragged groups without padding): the operand of fp8_matmul_wgrad, in the
+ * layout of fp4_to_fp8_cols.
+ *   x : bf16 [M, K] (M tokens, K features);  yT : uint8 [K, M], yT_scale :
+ *   float [cap, K], group_offsets, G, cap, dev_status : as in fp4_to_fp8_cols,
+ *   but offsets[G] <= M is enough (group_offsets NULL with G = 1: all M
+ *   tokens); codes of tokens that belong to no group and scale rows past the
+ *   last block are written as 0.
+ * A block is up to 128 tokens of one group and one feature, quantized by the
+ * rule of fp8_quantize_1x128.  Requires K > 0, K % 8 == 0, 1 <= G <=
+ * FQ_COLS_MAX_GROUPS, 0 <= M < 2^31 - 512.
+ */
+fq_status fp8_quantize_cols(const void *x, int64_t M, int64_t K, const int64_t *group_offsets,
+                            int32_t G, uint8_t *yT, float *yT_scale, int64_t cap,
+                            int32_t *dev_status, void *stream);
+
+/*
+ * Weight gradients from transposed FP8 operands ([MoE-FP4] 2.3: the
+ * transposed layout is the Wgrad operand), one per group:
+ *   aT : uint8 [N, M], aT_scale : float [cap, N]  (output gradients)
+ *   bT : uint8 [K, M], bT_scale : float [cap, K]  (activations)
+ *        both as fp8_quantize_cols, fp4_to_fp8_cols or bf16_to_mxfp4_fp8 write
+ *        them for the same group_offsets, G, cap (see there; offsets[G] <= M;
+ *        NULL with G = 1: all M tokens)
+ *   c  : [G, N, K] BF16 (c_f32 = 0) or FP32 (c_f32 = 1), output
+ *   c[g, n, k] = sum over the 128-token blocks b of group g of
+ *                aT_scale[b, n] bT_scale[b, k] *
+ *                sum over tokens t in b of  aT[n, t] bT[k, t]
+ * sums in binary32, rounded once.  An empty group's gradient is 0.
+ * accumulate = 1 adds to what c holds instead (an empty group's stays).
+ *   workspace : device memory of at least fp8_matmul_wgrad_workspace(M, N, K,
+ *        G) bytes, 16-byte aligned, overwritten; the operands are re-laid there
+ *        block by block (-1 for a rejected shape)
+ *   dev_status : as in fp8_matmul
+ * Requires N, K > 0 (K % 8 == 0 stores 16 bytes at a time), 1 <= G <=
+ * FQ_COLS_MAX_GROUPS, 0 <= M, cap >= fp4_to_fp8_cols_scale_capacity(M, G),
+ * 128 cap < 2^31 - 512.  Enqueues two kernels.  The same inputs give the same
+ * bits.
+ */
+int64_t fp8_matmul_wgrad_workspace(int64_t M, int64_t N, int64_t K, int32_t G);
+fq_status fp8_matmul_wgrad(const uint8_t *aT, const float *aT_scale, int64_t N, const uint8_t *bT,
+                           const float *bT_scale, int64_t K, int64_t M,
+                           const int64_t *group_offsets, int32_t G, int64_t cap, void *c,
+                           int c_f32, int accumulate, void *workspace, int64_t workspace_bytes,
+                           int32_t *dev_status, void *stream);
+
+/* Largest k and largest number of expert groups of moe_route. */
+#define FQ_ROUTE_MAX_K 32
+#define FQ_ROUTE_MAX_GROUPS 32
+
+/*
+ * Routing of tokens to experts.
+ *   logits : [T, E] FP32 (logits_f32 = 1) or BF16 (0);  bias : float [E] or NULL
+ *   score  s_e = softmax over the row (sigmoid = 0) or 1 / (1 + exp(-l_e))
+ *   choice c_e = s_e + bias_e: the bias moves the choice, not the weights
+ *   n_groups > 1: the E experts form n_groups equal runs; a run scores the
+ *          sum of its group_top (1 or 2) largest choices (of the available
+ *          experts it has), and only the keep_groups best runs are open
+ *   ids    : int32 [T, k] (output) the k largest choices, largest first
+ *   weights: float [T, k] (output) scale * s of each, divided by the sum of the
+ *          k scores if renormalize = 1 (0 where that sum is 0)
+ * All in binary32; ties go to the lowest index.  Without a bias, softmax
+ * scores are compared before their division by the row's sum.  An expert
+ * whose logit is NaN or at or below BF16's lowest finite value (-0x1.FEp127:
+ * a mask of -inf or of either type's lowest value), or whose choice is NaN
+ * or -inf, is not available: its score is 0 and it is never chosen.  A slot
+ * that finds no expert gets id -1 and weight 0.  +inf counts as FLT_MAX.
+ * Requires 1 <= E <= FQ_COLS_MAX_GROUPS, 1 <= k <= min(E, FQ_ROUTE_MAX_K),
+ * n_groups dividing E, 1 <= keep_groups <= n_groups <= FQ_ROUTE_MAX_GROUPS.
+ */
+fq_status moe_route(const void *logits, int logits_f32, int64_t T, int32_t E, int32_t k,
+                    const float *bias, int sigmoid, int32_t n_groups, int32_t keep_groups,
+                    int32_t group_top, int renormalize, float scale, float *weights, int32_t *ids,
+                    void *stream);
+
+/*
+ * Gradient of moe_route's weights with respect to the logits, for the ids it
+ * chose (which are constants; an id outside [0, E) takes no part).
+ *   dweights : float [T, k];  dlogits : [T, E] in the logits' type (output)
+ * logits, sigmoid, renormalize and scale as given to moe_route.
+ */
+fq_status moe_route_backward(const void *logits, int logits_f32, int64_t T, int32_t E,
+                             const int32_t *ids, const float *dweights, int32_t k, int sigmoid,
+                             int renormalize, float scale, void *dlogits, void *stream);
+
+/*
+ * Rows ordered by expert, on the device: the group offsets and the row order
+ * of the ragged per-expert calls.
+ *   ids : int32 [n], the expert of each (token, choice) pair in row-major
+ *         order; an id outside [0, E) belongs to no expert
+ *   group_offsets : int64 [E+1] (output), offsets[E] = pairs with an expert
+ *   pair_of_row   : int32 [n] (output) the pair of each row, rows ordered by
+ *                   expert and within an expert by pair; -1 from offsets[E] on
+ *   row_of_pair   : int32 [n] (output) the inverse; -1 for a pair of no expert
+ * Requires 1 <= E <= FQ_COLS_MAX_GROUPS, 0 <= n < 2^31 - 512.
+ */
+fq_status moe_sort_rows(const int32_t *ids, int64_t n, int32_t E, int64_t *group_offsets,
+                        int32_t *pair_of_row, int32_t *row_of_pair, void *stream);
+
+/*
  * MXFP4 -> BF16 dequantization ([MoE-FP4] 2.1: an element's value is its
  * E2M1 value times 2^(e-127) of its block's UE8M0 scale byte e).
  *   q, s : MXFP4 [M, K/2], [M, K/32];  x : bf16 [M, K] (output)
