@@ -16,11 +16,35 @@ namespace fq {
 
 namespace {
 
-constexpr int kTileM = 128;      // rows of a tile (TMEM lanes)
-constexpr int kBlockK = 128;     // one scale block, one pipeline stage
-constexpr int kPromoteWarps = 8;
-constexpr int kMmThreads = (kPromoteWarps + 2) * 32;
-constexpr int kRaster = 16;      // row tiles walked together over the columns
+constexpr int kRowsM = 128;       // rows of c of a CTA (its TMEM lanes)
+constexpr int kBlockK = 128;      // one scale block, one pipeline stage
+constexpr int kPromoteWarps = 8;  // two warpgroups
+constexpr int kMmThreads = (kPromoteWarps + 4) * 32;
+// 384 threads x 168 registers at launch = 64512; 256 x 200 + 128 x 104 as well
+constexpr int kPromoteRegs = 200, kOtherRegs = 104;
+constexpr int kRaster = 8;        // row tiles walked together over the columns
+constexpr int kScaleBlocks = 4;   // blocks whose scales are fetched together
+constexpr int kBoxCols = 32;      // columns of c that a warp writes at once
+
+// kCtas CTAs work on a tile of 128 kCtas rows.  Columns of the tile: 256 for a
+// pair, 128 for one CTA.
+template <int kCtas>
+struct Shape {
+    static constexpr int bn = 128 * kCtas;
+    static constexpr int cols = bn / 2;               // of a promoting thread
+    static constexpr int a_bytes = kRowsM * kBlockK;  // of a stage of a CTA
+    static constexpr int b_rows = bn / kCtas;
+    static constexpr int b_bytes = b_rows * kBlockK;
+    static constexpr int stages = 5;
+};
+
+// Boxes of 32 rows x kBoxCols columns of c, staged by a warp.
+template <bool kF32>
+struct Box {
+    static constexpr int row = kBoxCols * (kF32 ? 4 : 2);
+    static constexpr int bytes = 32 * row;
+    static constexpr int count = kF32 ? 1 : 2;
+};
 
 // What the second operand's scales and the tiles are:
 //   kTileScale  forward, one scale per 128x128 weight tile
@@ -30,22 +54,17 @@ constexpr int kRaster = 16;      // row tiles walked together over the columns
 //               and block
 enum Mode { kTileScale, kRowScale, kWgrad };
 
-template <int BN>
-struct MmShape {
-    static constexpr int stages = BN == 256 ? 4 : 6;
-    static constexpr int a_bytes = kTileM * kBlockK;
-    static constexpr int b_bytes = BN * kBlockK;
-    static constexpr int cols = BN / 2;  // columns of a promoting thread
-};
-
-// Shared memory behind the operand stages.
-template <int BN>
+// Shared memory behind the operand stages and the staged output.
+template <int kCtas>
 struct MmTail {
-    uint64_t full[MmShape<BN>::stages], empty[MmShape<BN>::stages];
+    using S = Shape<kCtas>;
+    uint64_t full[S::stages], empty[S::stages];
     uint64_t acc_full[2], acc_empty[2];
+    uint64_t scale_full[2], scale_empty[2];
     uint32_t tmem;
     int32_t abort;
-    float col_scale[2][BN];
+    // column scales of two groups of kScaleBlocks blocks
+    alignas(16) float col_scale[2][kScaleBlocks][S::bn];
     // int32 off[G + 2], first[G + 2] follow
 };
 
@@ -84,16 +103,17 @@ __device__ __forceinline__ void tile_coords(int32_t idx, int32_t mt, int32_t nt,
     i = band * kRaster + r - j * rows;
 }
 
-template <Mode kMode, int BN>
+template <Mode kMode, int kCtas>
 __device__ __forceinline__ Tile tile_at(int32_t idx, const MmArgs &p, const int32_t *off,
                                         const int32_t *first, int32_t mt, int32_t nt)
 {
+    constexpr int kRows = kCtas * kRowsM, BN = Shape<kCtas>::bn;
     Tile t;
     int32_t i, j;
     if (kMode == kWgrad) {
         t.g = idx / (mt * nt);
         tile_coords(idx - t.g * mt * nt, mt, nt, i, j);
-        t.row = t.arow = i * kTileM;
+        t.row = t.arow = i * kRows;
         t.n0 = t.brow = j * BN;
         t.end = p.R;
         t.blocks = first[t.g + 1] - first[t.g];
@@ -101,7 +121,7 @@ __device__ __forceinline__ Tile tile_at(int32_t idx, const MmArgs &p, const int3
     } else {
         tile_coords(idx, mt, nt, i, j);
         t.g = group_of_tile(first, p.G + 1, i);
-        t.row = t.arow = off[t.g] + (i - first[t.g]) * kTileM;
+        t.row = t.arow = off[t.g] + (i - first[t.g]) * kRows;
         t.n0 = j * BN;
         t.brow = t.g * p.N + t.n0;
         t.end = off[t.g + 1];
@@ -111,292 +131,517 @@ __device__ __forceinline__ Tile tile_at(int32_t idx, const MmArgs &p, const int3
     return t;
 }
 
-// Columns [col, col + 16) of one output row from 8 packed pairs; `fast` rows
-// are 16-byte aligned.
+// Byte of 16-byte piece i of row r in a box: the swizzle of a tensor copy of
+// rows of 64 (BF16) or 128 (FP32) bytes.
 template <bool kF32>
-__device__ __forceinline__ void store16(void *c, int64_t row_off, int32_t col, int32_t N, bool fast,
-                                        const uint64_t *acc)
+__device__ __forceinline__ int box_at(int r, int i)
 {
-    float v[16];
+    return Box<kF32>::row * r + 16 * (kF32 ? i ^ (r & 7) : i ^ ((r >> 1) & 3));
+}
+
+// A warp's box, from registers (lane l holds row l, packed pairs of columns).
+template <bool kF32>
+__device__ __forceinline__ void stage_box(uint8_t *box, const uint64_t *acc)
+{
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 8; i++)
-        unpack2(acc[i], v[2 * i], v[2 * i + 1]);
-    if (kF32) {
-        float *p = static_cast<float *>(c) + row_off + col;
-        if (fast && col + 16 <= N) {
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                reinterpret_cast<float4 *>(p)[i] =
-                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    for (int i = 0; i < Box<kF32>::row / 16; i++) {
+        uint4 *to = reinterpret_cast<uint4 *>(box + box_at<kF32>(lane, i));
+        float v[8];
+        if (kF32) {
+            unpack2(acc[2 * i], v[0], v[1]);
+            unpack2(acc[2 * i + 1], v[2], v[3]);
+            *to = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                             __float_as_uint(v[3]));
         } else {
 #pragma unroll
-            for (int i = 0; i < 16; i++)
-                if (col + i < N)
-                    p[i] = v[i];
-        }
-    } else {
-        uint16_t *p = static_cast<uint16_t *>(c) + row_off + col;
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            w[i] = cvt_bf16x2(v[2 * i], v[2 * i + 1]);
-        if (fast && col + 16 <= N) {
-            reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; i++)
-                if (col + i < N)
-                    p[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+            for (int h = 0; h < 4; h++)
+                unpack2(acc[4 * i + h], v[2 * h], v[2 * h + 1]);
+            *to = make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]),
+                             cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7]));
         }
     }
 }
 
-// acc += the 16 columns that c holds.
-template <bool kF32>
-__device__ __forceinline__ void add16(const void *c, int64_t row_off, int32_t col, int32_t N,
-                                      uint64_t *acc)
+// The staged box by ordinary stores, a row at a time: where the group's rows end
+// inside the box, where rows of c are not 16-byte aligned, and for c += box.
+template <bool kF32, bool kAdd>
+__device__ __forceinline__ void store_box(void *c, const uint8_t *box, int64_t row0, int32_t rows,
+                                          int32_t col, int32_t N)
+{
+    const int e = threadIdx.x & 31, b = e * (kF32 ? 4 : 2);
+    if (col + e >= N)
+        return;
+    for (int r = 0; r < rows; r++) {
+        const uint8_t *from = box + box_at<kF32>(r, b >> 4) + (b & 15);
+        const int64_t at = (row0 + r) * N + col + e;
+        if (kF32) {
+            float v = *reinterpret_cast<const float *>(from);
+            if (kAdd)
+                v += static_cast<float *>(c)[at];
+            static_cast<float *>(c)[at] = v;
+        } else {
+            static_cast<uint16_t *>(c)[at] = *reinterpret_cast<const uint16_t *>(from);
+        }
+    }
+}
+
+// acc += the BF16 values c holds (before the one rounding).
+template <int kCols>
+__device__ __forceinline__ void add_bf16(const void *c, int64_t row_off, int32_t col, int32_t N,
+                                         uint64_t *acc)
 {
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
+    for (int i = 0; i < kCols / 2; i++) {
         float v[2];
         unpack2(acc[i], v[0], v[1]);
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const int64_t at = row_off + col + 2 * i + h;
+        for (int h = 0; h < 2; h++)
             if (col + 2 * i + h < N)
-                v[h] += kF32 ? static_cast<const float *>(c)[at]
-                             : bf16_lo(static_cast<const uint16_t *>(c)[at]);
-        }
+                v[h] += bf16_lo(static_cast<const uint16_t *>(c)[row_off + col + 2 * i + h]);
         acc[i] = pack2(__float_as_uint(v[0]), __float_as_uint(v[1]));
     }
 }
 
-// Persistent, one CTA per SM.  Warps 0-7 add up the scaled blocks (warp w:
-// TMEM lanes 32 (w mod 4).., columns BN/2 * (w / 4)..), warp 8 issues the
-// tensor copies, warp 9 the MMAs.  Two TMEM buffers of BN columns: the MMAs of
-// block b + 1 run while block b is scaled and added.
-template <int BN, Mode kMode, bool kF32>
+// The tiles of a cluster, in order: a lane works out one of the next 32, a
+// shuffle hands the next one to the warp (the divisions and the search for the
+// group take longer than a block).
+template <Mode kMode, int kCtas>
+struct TileWalk {
+    Tile mine;
+    int32_t idx, step, ntiles, mt, nt;
+    int32_t n;
+
+    __device__ __forceinline__ TileWalk(int32_t idx0, int32_t stride, int32_t rows, int32_t cols,
+                                        int32_t total)
+        : idx(idx0), step(stride), ntiles(total), mt(rows), nt(cols), n(0)
+    {
+    }
+    // Whether there is another tile; next() then returns it.
+    __device__ __forceinline__ bool more() const { return idx < ntiles; }
+    __device__ __forceinline__ Tile next(const MmArgs &p, const int32_t *off, const int32_t *first)
+    {
+        if ((n & 31) == 0) {
+            const int64_t at = idx + static_cast<int64_t>(threadIdx.x & 31) * step;
+            mine = tile_at<kMode, kCtas>(static_cast<int32_t>(min(at, static_cast<int64_t>(ntiles - 1))),
+                                         p, off, first, mt, nt);
+        }
+        Tile t;
+        const int src = n & 31;
+        t.g = __shfl_sync(0xffffffffu, mine.g, src);
+        t.row = __shfl_sync(0xffffffffu, mine.row, src);
+        t.n0 = __shfl_sync(0xffffffffu, mine.n0, src);
+        t.end = __shfl_sync(0xffffffffu, mine.end, src);
+        t.blocks = __shfl_sync(0xffffffffu, mine.blocks, src);
+        t.xblk = __shfl_sync(0xffffffffu, mine.xblk, src);
+        t.arow = __shfl_sync(0xffffffffu, mine.arow, src);
+        t.brow = __shfl_sync(0xffffffffu, mine.brow, src);
+        n++;
+        idx = idx > ntiles - step ? ntiles : idx + step;
+        return t;
+    }
+};
+
+// The scales of one line (a row of c, a column or a weight tile) for up to
+// kScaleBlocks consecutive blocks, `step` floats apart, from `s` on; `vec`: the
+// four are one aligned vector.
+__device__ __forceinline__ float4 load_scales(const float *s, int64_t step, int32_t n, bool vec)
+{
+    if (vec)
+        return __ldg(reinterpret_cast<const float4 *>(s));
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (n > 0)
+        v.x = __ldg(s);
+    if (n > 1)
+        v.y = __ldg(s + step);
+    if (n > 2)
+        v.z = __ldg(s + 2 * step);
+    if (n > 3)
+        v.w = __ldg(s + 3 * step);
+    return v;
+}
+
+// Persistent: one CTA per SM, in clusters of kCtas.  Every CTA loads 128 rows of
+// a and its share of the rows of b per block and owns 128 rows of the
+// accumulator.  Warps 0-7 add up the scaled blocks (warp w: TMEM lanes 32 (w mod
+// 4).., half w / 4 of the columns), warp 8 issues the tensor copies, warp 9 of
+// the cluster's first CTA the MMAs, warp 10 fetches the scales of the columns
+// where every column has its own.  Two TMEM buffers: the MMAs of block b + 1 run while block b is
+// scaled and added.
+template <int kCtas, Mode kMode, bool kF32>
 __global__ void __launch_bounds__(kMmThreads, 1)
     fp8_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-                      const MmArgs p)
+                      const __grid_constant__ CUtensorMap tc, const MmArgs p)
 {
-    using S = MmShape<BN>;
+    using S = Shape<kCtas>;
+    using B = Box<kF32>;
+    constexpr int BN = S::bn, kCols = S::cols, kStages = S::stages;
+    constexpr int kTmemCols = 256 * kCtas, kBufCols = kTmemCols / 2;
     constexpr bool kColScale = kMode != kTileScale;
+    constexpr int kCopyWarp = kPromoteWarps, kMmaWarp = kCopyWarp + 1, kColWarp = kMmaWarp + 1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t *sA = smem, *sB = smem + S::stages * S::a_bytes;
-    MmTail<BN> &t = *reinterpret_cast<MmTail<BN> *>(sB + S::stages * S::b_bytes);
+    uint8_t *sA = smem, *sB = sA + kStages * S::a_bytes, *sC = sB + kStages * S::b_bytes;
+    MmTail<kCtas> &t =
+        *reinterpret_cast<MmTail<kCtas> *>(sC + kPromoteWarps * B::count * B::bytes);
     int32_t *off = reinterpret_cast<int32_t *>(&t + 1), *first = off + p.G + 2;
 
     const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (wid == 9) {
+    const uint32_t rank = kCtas == 1 ? 0 : cluster_rank();
+    if (wid == kMmaWarp) {
         if (lane == 0) {
-            for (int i = 0; i < S::stages; i++) {
+            for (int i = 0; i < kStages; i++) {
                 mbar_init(&t.full[i], 1);
                 mbar_init(&t.empty[i], 1);
             }
             for (int i = 0; i < 2; i++) {
                 mbar_init(&t.acc_full[i], 1);
-                mbar_init(&t.acc_empty[i], kPromoteWarps);
+                mbar_init(&t.acc_empty[i], kCtas * kPromoteWarps);
+                mbar_init(&t.scale_full[i], 1);
+                mbar_init(&t.scale_empty[i], kPromoteWarps);
             }
             t.abort = 0;
             mbar_init_fence();
         }
         __syncwarp();
-        tmem_alloc(&t.tmem, 2 * BN);
+        tmem_alloc<kCtas>(&t.tmem, kTmemCols);
     }
     griddep_wait();  // the previous kernel's outputs (PDL launch)
     if (wid == 0) {
-        const bool bad = load_row_groups(p.offs, p.G, p.M, kTileM, off, first);
+        const bool bad = load_row_groups(p.offs, p.G, p.M, kMode == kWgrad ? 128 : kCtas * kRowsM,
+                                         off, first);
         if (bad && p.dev_status && blockIdx.x == 0 && lane == 0)
             atomicOr(p.dev_status, 1);
     }
     tc_fence_before();
     __syncthreads();
+    if (kCtas > 1) {  // the barriers of both CTAs are set up
+        cluster_arrive();
+        cluster_wait();
+    }
     tc_fence_after();
     const uint32_t tmem = t.tmem;
-    const int32_t mt = kMode == kWgrad ? (p.R + kTileM - 1) / kTileM : first[p.G + 1];
+    volatile int32_t *abort = &t.abort;
+    const int32_t mt = kMode == kWgrad ? (p.R + kCtas * kRowsM - 1) / (kCtas * kRowsM)
+                                       : first[p.G + 1];
     const int32_t nt = (p.N + BN - 1) / BN;
     const int32_t ntiles = mt * nt * (kMode == kWgrad ? p.G : 1);
+    TileWalk<kMode, kCtas> walk(blockIdx.x / kCtas, gridDim.x / kCtas, mt, nt, ntiles);
 
-    if (wid == 8) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int32_t idx = blockIdx.x; ok && idx < ntiles; idx += gridDim.x) {
-                const Tile tl = tile_at<kMode, BN>(idx, p, off, first, mt, nt);
-                for (int32_t b = 0; b < tl.blocks; b++, it++) {
-                    const uint32_t s = it % S::stages, ph = (it / S::stages) & 1;
-                    if (!(ok = mbar_wait_or_abort(&t.empty[s], ph ^ 1, &t.abort)))
+    if (wid >= kPromoteWarps) {
+        regs_down<kOtherRegs>();
+        if (wid == kCopyWarp) {
+            const uint32_t full0 = smem_u32(t.full), empty0 = smem_u32(t.empty);
+            const uint32_t fill0 = kCtas == 1 ? full0 : cluster_addr(t.full, 0);
+            const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
+            uint32_t s = 0, ph = 1;
+            while (!*abort && walk.more()) {
+                const Tile tl = walk.next(p, off, first);
+                const int32_t arow = tl.arow + rank * kRowsM, brow = tl.brow + rank * S::b_rows;
+                int32_t x = tl.xblk * kBlockK;
+                for (int32_t b = 0; b < tl.blocks; b++, x += kBlockK) {
+                    warp_wait(empty0 + 8 * s, ph, abort);
+                    if (*abort)
                         break;
-                    mbar_arrive_expect_tx(&t.full[s], S::a_bytes + S::b_bytes);
-                    tma_load_2d(sA + s * S::a_bytes, &ta, (tl.xblk + b) * kBlockK, tl.arow, &t.full[s]);
-                    tma_load_2d(sB + s * S::b_bytes, &tb, (tl.xblk + b) * kBlockK, tl.brow, &t.full[s]);
+                    if (elect_one()) {
+                        if (rank == 0)
+                            mbar_arrive_expect_tx(&t.full[s], kCtas * (S::a_bytes + S::b_bytes));
+                        if (kCtas == 1) {
+                            tma_load_2d(sA + s * S::a_bytes, &ta, x, arow, &t.full[s]);
+                            tma_load_2d(sB + s * S::b_bytes, &tb, x, brow, &t.full[s]);
+                        } else {
+                            tma_load_2d_pair(a0 + s * S::a_bytes, &ta, x, arow, fill0 + 8 * s);
+                            tma_load_2d_pair(b0 + s * S::b_bytes, &tb, x, brow, fill0 + 8 * s);
+                        }
+                    }
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
                 }
             }
-            if (!ok)  // no copy may land after the CTA is gone
-                for (uint32_t k = it > S::stages ? it - S::stages : 0; k < it; k++)
-                    mbar_wait(&t.full[k % S::stages], (k / S::stages) & 1);
-        }
-        __syncwarp();
-    } else if (wid == 9) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_e4m3(kTileM, BN);
-            uint32_t it = 0;
-            bool ok = true;
-            for (int32_t idx = blockIdx.x; ok && idx < ntiles; idx += gridDim.x) {
-                const int32_t blocks = tile_at<kMode, BN>(idx, p, off, first, mt, nt).blocks;
+            // every stage has been consumed: the last arrivals of the MMAs, which
+            // come from the pair's first CTA, find this CTA's barriers
+            for (int k = 0; k < kStages; k++) {
+                warp_wait(empty0 + 8 * s, ph, abort);
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+            if (*abort) {  // no copy may land after the CTA is gone: a millisecond is plenty
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 1000000)
+                    ;
+            }
+        } else if (wid == kMmaWarp && rank == 0) {
+            constexpr uint32_t idesc = idesc_e4m3(kCtas * kRowsM, BN);
+            const uint64_t da0 = smem_desc_sw128(sA), db0 = smem_desc_sw128(sB);
+            const uint32_t full0 = smem_u32(t.full), empty0 = smem_u32(t.empty);
+            const uint32_t acc_full0 = smem_u32(t.acc_full), acc_empty0 = smem_u32(t.acc_empty);
+            uint32_t s = 0, ph = 0, it = 0;
+            uint64_t da = da0, db = db0;
+            while (!*abort && walk.more()) {
+                const int32_t blocks = walk.next(p, off, first).blocks;
                 for (int32_t b = 0; b < blocks; b++, it++) {
-                    const uint32_t s = it % S::stages, ph = (it / S::stages) & 1;
-                    const uint32_t buf = it & 1, bph = (it >> 1) & 1;
-                    if (!(ok = mbar_wait_or_abort(&t.acc_empty[buf], bph ^ 1, &t.abort) &&
-                               mbar_wait_or_abort(&t.full[s], ph, &t.abort)))
-                        break;
+                    const uint32_t buf = it & 1;
+                    warp_wait(full0 + 8 * s, ph, abort);
+                    warp_wait(acc_empty0 + 8 * buf, ((it >> 1) & 1) ^ 1, abort);
                     tc_fence_after();
-                    const uint64_t da = smem_desc_sw128(sA + s * S::a_bytes);
-                    const uint64_t db = smem_desc_sw128(sB + s * S::b_bytes);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kBlockK / 32; k++)
-                        mma_e4m3(tmem + buf * BN, da + 2 * k, db + 2 * k, idesc, k > 0);
-                    mma_commit(&t.empty[s]);
-                    mma_commit(&t.acc_full[buf]);
+                        for (int k = 0; k < kBlockK / 32; k++)
+                            mma_e4m3<kCtas>(tmem + buf * kBufCols, da + 2 * k, db + 2 * k, idesc, k > 0);
+                        mma_commit<kCtas>(acc_full0 + 8 * buf);
+                        mma_commit<kCtas>(empty0 + 8 * s);
+                    }
+                    s++;
+                    da += S::a_bytes >> 4;
+                    db += S::b_bytes >> 4;
+                    if (s == kStages) {
+                        s = 0;
+                        ph ^= 1;
+                        da = da0;
+                        db = db0;
+                    }
                 }
             }
-            if (!ok && it > 0)  // no MMA may be in flight when TMEM is freed
-                mbar_wait(&t.acc_full[(it - 1) & 1], ((it - 1) >> 1) & 1);
+            if (*abort) {  // no MMA may be in flight when TMEM is freed
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 1000000)
+                    ;
+            }
+        } else if (kColScale && wid == kColWarp) {
+            constexpr int kPer = BN / 32;  // columns of a lane
+            const bool vec = kMode == kRowScale && p.KB % 4 == 0;
+            uint32_t gq = 0;
+            while (!*abort && walk.more()) {
+                const Tile tl = walk.next(p, off, first);
+                for (int32_t b = 0; b < tl.blocks; b += kScaleBlocks, gq++) {
+                    const uint32_t slot = gq & 1;
+                    warp_wait(smem_u32(&t.scale_empty[slot]), ((gq >> 1) & 1) ^ 1, abort);
+#pragma unroll
+                    for (int i = 0; i < kPer; i += 2) {
+                        float4 v[2];
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            const int32_t col = min(tl.n0 + lane + 32 * (i + h), p.N - 1);
+                            const float *s =
+                                kMode == kWgrad
+                                    ? p.sb + static_cast<int64_t>(tl.xblk + b) * p.N + col
+                                    : p.sb + (static_cast<int64_t>(tl.g) * p.N + col) * p.KB + b;
+                            v[h] = load_scales(s, kMode == kWgrad ? p.N : 1, tl.blocks - b, vec);
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            float *to = &t.col_scale[slot][0][lane + 32 * (i + h)];
+                            to[0] = v[h].x;
+                            to[BN] = v[h].y;
+                            to[2 * BN] = v[h].z;
+                            to[3 * BN] = v[h].w;
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&t.scale_full[slot]);
+                }
+            }
         }
         __syncwarp();
     } else {
+        regs_up<kPromoteRegs>();
         const int half = wid >> 2;
-        const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * (wid & 3)) << 16) + half * S::cols;
-        const int esize = kF32 ? 4 : 2;
-        const bool fast = (static_cast<int64_t>(p.N) * esize) % 16 == 0;
-        uint32_t it = 0;
-        bool ok = true;
-        for (int32_t idx = blockIdx.x; ok && idx < ntiles; idx += gridDim.x) {
-            const Tile tl = tile_at<kMode, BN>(idx, p, off, first, mt, nt);
-            const int32_t row = tl.row + 32 * (wid & 3) + lane;
-            const bool in = row < tl.end;
-            uint64_t acc[S::cols / 2];
+        const uint32_t lane_base =
+            tmem + (static_cast<uint32_t>(32 * (wid & 3)) << 16) + half * kCols;
+        const bool aligned = static_cast<int64_t>(p.N) * (kF32 ? 4 : 2) % 16 == 0;
+        uint8_t *stage = sC + wid * B::count * B::bytes;
+        const bool leader = lane == 0;
+        const uint32_t acc_full0 = smem_u32(t.acc_full);
+        const uint32_t read0 = kCtas == 1 ? smem_u32(t.acc_empty) : cluster_addr(t.acc_empty, 0);
+        const uint32_t scale_full0 = smem_u32(t.scale_full), scale_empty0 = smem_u32(t.scale_empty);
+        uint32_t it = 0, gq = 0, nbox = 0;
+        while (!*abort && walk.more()) {
+            const Tile tl = walk.next(p, off, first);
+            const int32_t blocks = tl.blocks;
+            const int32_t col0 = tl.n0 + half * kCols;
+            const int32_t row0 = tl.row + rank * kRowsM + 32 * (wid & 3);
+            uint64_t acc[kCols / 2];
 #pragma unroll
-            for (int e = 0; e < S::cols / 2; e++)
+            for (int e = 0; e < kCols / 2; e++)
                 acc[e] = 0;
-            if (tl.blocks > 0) {
-                // scales of the row and of the column (or weight tile), and
-                // their distance from block to block
-                const int32_t col = tl.n0 + (kColScale ? static_cast<int32_t>(threadIdx.x) % BN
-                                                       : half * S::cols);
-                const int64_t sa_step = kMode == kWgrad ? p.R : 1;
-                const int64_t sb_step = kMode == kWgrad ? p.N : 1;
-                const float *sa, *sb;
-                if (kMode == kWgrad) {
-                    sa = p.sa + static_cast<int64_t>(tl.xblk) * p.R + min(row, p.R - 1);
-                    sb = p.sb + static_cast<int64_t>(tl.xblk) * p.N + min(col, p.N - 1);
-                } else {
-                    sa = p.sa + static_cast<int64_t>(min(row, p.M - 1)) * p.KB;
-                    sb = p.sb + (static_cast<int64_t>(tl.g) * p.sb_rows +
-                                 min(kColScale ? col : col / 128, p.sb_rows - 1)) * p.KB;
+            // the scales of the row and (kTileScale) of the weight tile that the
+            // columns lie in, fetched two blocks ahead
+            const int64_t step = kMode == kWgrad ? p.R : 1;
+            const float *sa = kMode == kWgrad
+                                  ? p.sa + static_cast<int64_t>(tl.xblk) * p.R + min(row0 + lane, p.R - 1)
+                                  : p.sa + static_cast<int64_t>(min(row0 + lane, p.M - 1)) * p.KB;
+            const float *sb = p.sb + (static_cast<int64_t>(tl.g) * p.sb_rows +
+                                      min(col0 / 128, p.sb_rows - 1)) * p.KB;
+            float a0 = 0.0f, a1 = 0.0f, b0 = 1.0f, b1 = 1.0f;
+            if (blocks > 0) {
+                a0 = __ldg(sa);
+                if (!kColScale)
+                    b0 = __ldg(sb);
+            }
+            if (blocks > 1) {
+                a1 = __ldg(sa + step);
+                if (!kColScale)
+                    b1 = __ldg(sb + 1);
+            }
+            sa += 2 * step;
+            sb += 2;
+            // A wait that gives up does not leave the loop (the other warps' waits
+            // end soon as well); the flag is looked at behind it.
+#pragma unroll 1
+            for (int32_t b = 0; b < blocks; b++, it++) {
+                const float s = kColScale ? a0 : a0 * b0;
+                a0 = a1;
+                b0 = b1;
+                if (b + 2 < blocks) {
+                    a1 = __ldg(sa);
+                    sa += step;
+                    if (!kColScale)
+                        b1 = __ldg(sb++);
                 }
-                float a0 = __ldg(sa), b0 = __ldg(sb);
-                float a1 = tl.blocks > 1 ? __ldg(sa + sa_step) : 0.0f;
-                float b1 = tl.blocks > 1 ? __ldg(sb + sb_step) : 0.0f;
-                sa += 2 * sa_step;
-                sb += 2 * sb_step;
-                for (int32_t b = 0; b < tl.blocks; b++, it++) {
-                    const float scale = kColScale ? a0 : a0 * b0;
-                    const float col_scale = b0;
-                    a0 = a1;
-                    b0 = b1;
-                    if (b + 2 < tl.blocks) {
-                        a1 = __ldg(sa);
-                        b1 = __ldg(sb);
-                        sa += sa_step;
-                        sb += sb_step;
-                    }
-                    const uint32_t buf = it & 1, bph = (it >> 1) & 1;
-                    if (kColScale) {
-                        if (threadIdx.x < BN)
-                            t.col_scale[buf][threadIdx.x] = col_scale;
-                        // a wait that gave up in one warp is known to all of them
-                        // here: they leave the tile loop together
-                        ok = !named_barrier_or(1, kPromoteWarps * 32, !ok);
-                    }
-                    ok = ok && mbar_wait_or_abort(&t.acc_full[buf], bph, &t.abort);
-                    tc_fence_after();
-                    const uint64_t sc = pack2(__float_as_uint(scale), __float_as_uint(scale));
-                    const uint32_t addr = lane_base + buf * BN;
-                    uint32_t r[2][16];
-                    tmem_ld16(addr, r[0]);
+                const uint32_t buf = it & 1, slot = gq & 1;
+                const float *cols = &t.col_scale[slot][b % kScaleBlocks][half * kCols];
+                if (kColScale && b % kScaleBlocks == 0)
+                    warp_wait(scale_full0 + 8 * slot, (gq >> 1) & 1, abort);
+                warp_wait(acc_full0 + 8 * buf, (it >> 1) & 1, abort);
+                tc_fence_after();
+                const uint64_t sc = pack2(__float_as_uint(s), __float_as_uint(s));
+                const uint32_t addr = lane_base + buf * kBufCols;
 #pragma unroll
-                    for (int c = 0; c < S::cols / 16; c++) {
-                        tmem_wait_ld(r[c & 1]);
-                        if (c + 1 < S::cols / 16)
-                            tmem_ld16(addr + 16 * (c + 1), r[(c + 1) & 1]);
+                for (int c = 0; c < kCols / 32; c++) {
+                    uint32_t r[32];
+                    tmem_ld32(addr + 32 * c, r);
+                    tmem_wait_ld();
+                    if (c + 1 == kCols / 32) {  // the buffer has been read
+                        tc_fence_before();
+                        mbar_arrive_cluster(read0 + 8 * buf, leader);
+                    }
+                    uint64_t *o = acc + 16 * c;
 #pragma unroll
-                        for (int e = 0; e < 8; e++) {
-                            uint64_t v = pack2(r[c & 1][2 * e], r[c & 1][2 * e + 1]);
-                            if (kColScale) {
-                                const float2 cs = *reinterpret_cast<const float2 *>(
-                                    &t.col_scale[buf][half * S::cols + 16 * c + 2 * e]);
-                                v = mul2(v, pack2(__float_as_uint(cs.x), __float_as_uint(cs.y)));
-                            }
-                            acc[8 * c + e] = fma2(v, sc, acc[8 * c + e]);
+                    for (int e = 0; e < 32; e += 4) {
+                        if (kColScale) {
+                            const uint4 cs =
+                                *reinterpret_cast<const uint4 *>(cols + 32 * c + e);
+                            mul_fma2(o[e / 2], r[e], r[e + 1], cs.x, cs.y, sc);
+                            mul_fma2(o[e / 2 + 1], r[e + 2], r[e + 3], cs.z, cs.w, sc);
+                        } else {
+                            fma2(o[e / 2], r[e], r[e + 1], sc);
+                            fma2(o[e / 2 + 1], r[e + 2], r[e + 3], sc);
                         }
                     }
-                    tc_fence_before();
+                }
+                if (kColScale && (b % kScaleBlocks == kScaleBlocks - 1 || b + 1 == blocks)) {
                     __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&t.acc_empty[buf]);
+                    mbar_arrive_cluster(scale_empty0 + 8 * slot, leader);
+                    gq++;
                 }
             }
-            if (kColScale)
-                ok = !named_barrier_or(1, kPromoteWarps * 32, !ok);
-            if (in && ok) {
-                const int64_t row_off =
-                    ((kMode == kWgrad ? static_cast<int64_t>(tl.g) * p.R : 0) + row) * p.N;
+            const bool ok = __all_sync(0xffffffffu, *abort == 0);
+            const int32_t rows = min(32, tl.end - row0);
+            if (ok && rows > 0) {
+                const int64_t out0 = (kMode == kWgrad ? static_cast<int64_t>(tl.g) * p.R : 0) + row0;
+                const bool add = kMode == kWgrad && p.add;
+                const bool bulk = aligned && rows == 32 && !add;
+                if (!kF32 && add && lane < rows)
+                    add_bf16<kCols>(p.c, (out0 + lane) * p.N, col0, p.N, acc);
 #pragma unroll
-                for (int c = 0; c < S::cols / 16; c++) {
-                    const int32_t col = tl.n0 + half * S::cols + 16 * c;
-                    if (col < p.N) {
-                        if (kMode == kWgrad && p.add)
-                            add16<kF32>(p.c, row_off, col, p.N, acc + 8 * c);
-                        store16<kF32>(p.c, row_off, col, p.N, fast, acc + 8 * c);
+                for (int x = 0; x < kCols / kBoxCols; x++) {
+                    const int32_t col = col0 + kBoxCols * x;
+                    if (col >= p.N)
+                        continue;
+                    // the box used B::count boxes ago has been read
+                    uint8_t *box = stage + nbox % B::count * B::bytes;
+                    nbox++;
+                    if (lane == 0)
+                        tma_store_wait_read<B::count - 1>();
+                    __syncwarp();
+                    stage_box<kF32>(box, acc + kBoxCols / 2 * x);
+                    fence_async_shared();
+                    __syncwarp();
+                    if (!bulk) {
+                        if (add)
+                            store_box<kF32, true>(p.c, box, out0, rows, col, p.N);
+                        else
+                            store_box<kF32, false>(p.c, box, out0, rows, col, p.N);
+                        __syncwarp();
+                    }
+                    if (lane == 0) {
+                        if (bulk)
+                            tma_store_2d(&tc, box, col, static_cast<int32_t>(out0));
+                        tma_store_commit();  // a group for every box
                     }
                 }
             }
         }
+        if (lane == 0)
+            tma_store_wait();
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
-    if (wid == 9)
-        tmem_free(tmem, 2 * BN);
+    if (kCtas > 1) {  // nothing of the pair reaches into this CTA any more
+        cluster_arrive();
+        cluster_wait();
+    }
+    if (wid == kMmaWarp)
+        tmem_free<kCtas>(tmem, kTmemCols);
     if (threadIdx.x == 0 && t.abort && p.dev_status)
         atomicOr(p.dev_status, 2);
 }
 
 // Both operands: [rows, K bytes] matrices cut into 128-byte blocks along K.
-template <int BN, Mode kMode, bool kF32>
+template <int kCtas, Mode kMode, bool kF32>
 fq_status launch_matmul(const uint8_t *a, int64_t a_rows, const uint8_t *b, int64_t b_rows,
-                        int64_t K, int64_t tiles, const MmArgs &p, cudaStream_t st)
+                        int64_t K, int64_t c_rows, const MmArgs &p, cudaStream_t st)
 {
-    CUtensorMap ta, tb;
-    if (!encode_tensor_map_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, a, K, a_rows, K, kBlockK, kTileM,
-                              CU_TENSOR_MAP_SWIZZLE_128B, true) ||
-        !encode_tensor_map_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, b, K, b_rows, K, kBlockK, BN,
-                              CU_TENSOR_MAP_SWIZZLE_128B, true)) {
+    using S = Shape<kCtas>;
+    using B = Box<kF32>;
+    constexpr int kSize = kF32 ? 4 : 2;
+    CUtensorMap ta, tb, tc = {};
+    bool ok = encode_tensor_map_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, a, K, a_rows, K, kBlockK,
+                                   kRowsM, CU_TENSOR_MAP_SWIZZLE_128B, true) &&
+              encode_tensor_map_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, b, K, b_rows, K, kBlockK,
+                                   S::b_rows, CU_TENSOR_MAP_SWIZZLE_128B, true);
+    if (static_cast<int64_t>(p.N) * kSize % 16 == 0)  // otherwise c is not written by tensor copies
+        ok = ok && encode_tensor_map_2d(&tc, kF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                        p.c, p.N, c_rows, static_cast<uint64_t>(p.N) * kSize,
+                                        kBoxCols, 32, kF32 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                           : CU_TENSOR_MAP_SWIZZLE_64B, false);
+    if (!ok) {
         set_last_cuda_error(static_cast<int>(cudaErrorNotSupported));
         return FQ_ERR_CUDA;
     }
-    using S = MmShape<BN>;
-    const auto kern = fp8_matmul_kernel<BN, kMode, kF32>;
-    const size_t dyn = 1024 + S::stages * (S::a_bytes + S::b_bytes) + sizeof(MmTail<BN>) +
+    const auto kern = fp8_matmul_kernel<kCtas, kMode, kF32>;
+    const size_t dyn = 1024 + S::stages * (S::a_bytes + S::b_bytes) +
+                       kPromoteWarps * B::count * B::bytes + sizeof(MmTail<kCtas>) +
                        2 * (p.G + 2) * sizeof(int32_t);
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(dyn)) != cudaSuccess)
         return launch_status();
-    const int grid = static_cast<int>(tiles < sm_count() ? tiles : sm_count());
-    if (launch_pdl(kern, dim3(grid), dim3(kMmThreads), dyn, st, ta, tb, p) != cudaSuccess)
+    const int64_t rows = kCtas * kRowsM, nt = (p.N + S::bn - 1) / S::bn;
+    const int64_t tiles = kMode == kWgrad ? (p.R + rows - 1) / rows * nt * p.G
+                                          : ((p.M + rows - 1) / rows + p.G + 1) * nt;
+    const int64_t most = sm_count() / kCtas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(kCtas * (tiles < most ? tiles : most)));
+    cfg.blockDim = dim3(kMmThreads);
+    cfg.dynamicSmemBytes = dyn;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCtas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kern, ta, tb, tc, p) != cudaSuccess)
         return launch_status();
     return launch_status();
 }
@@ -505,12 +750,11 @@ extern "C" fq_status fp8_matmul(const uint8_t *a, const float *sa, int64_t M, in
     p.KB = static_cast<int32_t>(K / 128);
     p.sb_rows = b_block == 1 ? p.N : (p.N + 127) / 128;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t tiles = ((M + kTileM - 1) / kTileM + G + 1) * ((N + 255) / 256);
     if (b_block == 1)
-        return c_f32 ? launch_matmul<256, kRowScale, true>(a, M, b, G * N, K, tiles, p, st)
-                     : launch_matmul<256, kRowScale, false>(a, M, b, G * N, K, tiles, p, st);
-    return c_f32 ? launch_matmul<256, kTileScale, true>(a, M, b, G * N, K, tiles, p, st)
-                 : launch_matmul<256, kTileScale, false>(a, M, b, G * N, K, tiles, p, st);
+        return c_f32 ? launch_matmul<2, kRowScale, true>(a, M, b, G * N, K, M, p, st)
+                     : launch_matmul<2, kRowScale, false>(a, M, b, G * N, K, M, p, st);
+    return c_f32 ? launch_matmul<2, kTileScale, true>(a, M, b, G * N, K, M, p, st)
+                 : launch_matmul<2, kTileScale, false>(a, M, b, G * N, K, M, p, st);
 }
 
 extern "C" int64_t fp8_matmul_wgrad_workspace(int64_t M, int64_t N, int64_t K, int32_t G)
@@ -536,8 +780,8 @@ extern "C" fq_status fp8_matmul_wgrad(const uint8_t *aT, const float *aT_scale, 
     if (G < 1 || G > FQ_COLS_MAX_GROUPS || (c_f32 != 0 && c_f32 != 1) ||
         (accumulate != 0 && accumulate != 1) || (!group_offsets && G != 1))
         return FQ_ERR_ARG;
-    const int64_t mt = (N + kTileM - 1) / kTileM, nt = (K + 255) / 256;
-    if (need < 0 || mt > INT32_MAX / nt / G)
+    const int64_t mt = (N + 127) / 128, nt = (K + 127) / 128;
+    if (need < 0 || mt > INT32_MAX / nt / G || N > INT32_MAX / G)  // 32-bit tiles and rows of c
         return FQ_ERR_SHAPE;
     if (cap < fp4_to_fp8_cols_scale_capacity(M, G) || workspace_bytes < need)
         return FQ_ERR_ARG;
@@ -567,8 +811,7 @@ extern "C" fq_status fp8_matmul_wgrad(const uint8_t *aT, const float *aT_scale, 
     p.R = static_cast<int32_t>(N);
     p.N = static_cast<int32_t>(K);
     p.add = accumulate;
-    const int64_t tiles = mt * nt * G;
     const uint8_t *wb = ws + N * pitch;
-    return c_f32 ? launch_matmul<256, kWgrad, true>(ws, N, wb, K, pitch, tiles, p, st)
-                 : launch_matmul<256, kWgrad, false>(ws, N, wb, K, pitch, tiles, p, st);
+    return c_f32 ? launch_matmul<2, kWgrad, true>(ws, N, wb, K, pitch, G * N, p, st)
+                 : launch_matmul<2, kWgrad, false>(ws, N, wb, K, pitch, G * N, p, st);
 }

@@ -16,7 +16,7 @@
 #include <cfloat>
 #include <cmath>
 
-#include "fq_common.cuh"
+#include "fq_tc.cuh"
 
 namespace fq {
 
@@ -313,32 +313,11 @@ __global__ void __launch_bounds__(kThreads) moe_route_backward_kernel(const Rout
 
 // ---------------------------------------------------------------- rows by expert
 
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size()
-{
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive()
-{
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait()
-{
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
 // A 32-bit word of another CTA's shared memory, by the address of one's own.
 __device__ __forceinline__ uint32_t ld_cluster(const uint32_t *own, uint32_t rank)
 {
-    uint32_t a, v;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(own)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(own, rank)) : "memory");
     return v;
 }
 

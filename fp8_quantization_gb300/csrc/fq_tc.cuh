@@ -8,42 +8,84 @@ namespace fq {
 
 // ---------------------------------------------------------------- bounded waits
 
-// Waits for phase `parity` of `bar` at most kWaitLimitNs; a wait that runs out
-// raises the CTA's shared `abort` flag, at which every other wait of the CTA
-// gives up too, so that all roles reach the kernel's end.
-__device__ __forceinline__ bool mbar_wait_or_abort(uint64_t *bar, uint32_t parity,
-                                                   volatile int32_t *abort)
+// A whole converged warp waits for phase `parity` of the mbarrier at shared
+// address `bar`, at most about kWaitLimitNs; a wait that runs out raises the
+// CTA's shared `abort` flag, at which every other wait of the CTA gives up too,
+// so that all roles reach the kernel's end.  Every branch is on a vote of the
+// warp: branches on which the lanes could part cost about 100 cycles here.
+__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, volatile int32_t *abort)
 {
-    if (mbar_try_wait(bar, parity))
-        return true;
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (*abort)
-            return false;
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
-            *abort = 1;
-            return false;
+    auto done = [&]() {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(bar), "r"(parity)
+                     : "memory");
+        return __all_sync(0xffffffffu, ok);
+    };
+    uint64_t t0 = 0;
+    for (uint32_t n = 1; !done(); n++) {
+        if (n % 64 == 0) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0)
+                t0 = now;
+            if (__any_sync(0xffffffffu, *abort != 0 || now - t0 > kWaitLimitNs)) {
+                *abort = 1;
+                return;
+            }
         }
     }
-    return true;
+}
+
+// One lane of the converged warp, always the same.  The tensor copies and
+// tcgen05 instructions take their operands from the warp's uniform registers:
+// behind this predicate the compiler knows that one thread issues them, behind
+// a comparison of lane numbers it does not.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "elect.sync _|p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r));
+    return r != 0;
 }
 
 // ---------------------------------------------------------------- tcgen05
 
+// kCtas = 1: the CTA alone; kCtas = 2: a cluster of two CTAs whose tensor cores
+// work on one tile (each CTA holds its half of both operands and of the
+// accumulator rows; the CTA of even rank issues).
+
 // Columns of TMEM for the CTA (a power of two, 32..512); the base address is
-// written to shared memory.  One full warp allocates and later frees.
+// written to shared memory.  One full warp (of each CTA) allocates and frees.
+template <int kCtas>
 __device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t cols)
 {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(dst)),
-                 "r"(cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if (kCtas == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(dst)),
+                     "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(dst)),
+                     "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
 }
 
+template <int kCtas>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols)
 {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+    if (kCtas == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -68,46 +110,164 @@ constexpr uint32_t idesc_e4m3(int m, int n)
 
 // D (+)= A B^T over 32 elements of K, issued by one thread; `accumulate`
 // false starts a new sum.
+template <int kCtas>
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          bool accumulate)
 {
+    const uint32_t acc = accumulate;
+    if (kCtas == 1)
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "setp.ne.u32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(idesc), "r"(acc)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "setp.ne.u32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(idesc), "r"(acc)
+                     : "memory");
+}
+
+// One arrival on the barrier at shared address `bar` (kCtas = 2: on the barrier
+// at that place in both CTAs) once every tcgen05.mma this thread issued is done.
+template <int kCtas>
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    if (kCtas == 1)
+        asm volatile(
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+                     ".multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                     "h"(static_cast<uint16_t>(3))
+                     : "memory");
+}
+
+// ---------------------------------------------------------------- clusters
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Address, in the cluster's shared memory, of CTA `rank`'s object at the place
+// of this CTA's `own`.
+__device__ __forceinline__ uint32_t cluster_addr(const void *own, uint32_t rank)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(own)), "r"(rank));
+    return a;
+}
+
+// An arrival by the lanes with `pred`, on a barrier of this CTA or its pair's
+// (released to the CTA only: a cluster-wide release costs the length of a block,
+// and what it would order, the TMEM reads, has its own fences).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar, bool pred)
+{
     asm volatile("{\n\t.reg .pred p;\n\t"
-                 "setp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+                 "setp.ne.u32 p, %1, 0;\n\t"
+                 "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
+                 "r"(static_cast<uint32_t>(pred))
                  : "memory");
 }
 
-// One arrival on `bar` once every tcgen05.mma this thread issued has finished.
-__device__ __forceinline__ void mma_commit(uint64_t *bar)
+// 2D tensor copy into this CTA's shared memory that completes on the barrier
+// at `bar`, this CTA's or its pair's.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, int32_t x,
+                                                 int32_t y, uint32_t bar)
 {
     asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-            smem_u32(bar))
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
 
-// 16 consecutive FP32 columns of the warp's 32 TMEM lanes (lane i of the warp
-// reads lane 32 (warp mod 4) + i); valid after tmem_wait_ld().
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16])
+// 2D tensor copy from shared memory to global memory (rows and columns outside
+// the tensor are not written), in the thread's current group of such copies.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int32_t x,
+                                             int32_t y)
 {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15])
-        : "r"(addr));
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::
+                     "l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(x), "r"(y)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_store_commit()
+{
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// All but the thread's last `kPending` groups have been read from shared memory.
+template <int kPending>
+__device__ __forceinline__ void tma_store_wait_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
+}
+// All of the thread's groups are done.
+__device__ __forceinline__ void tma_store_wait()
+{
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+// Makes the thread's shared-memory writes visible to tensor copies.
+__device__ __forceinline__ void fence_async_shared()
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Waits for the warp's TMEM loads; the loaded registers pass through it so
-// that no use of them is scheduled ahead of the wait.
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16])
+// ---------------------------------------------------------------- TMEM reads
+
+// 32 consecutive FP32 columns of the warp's 32 TMEM lanes (lane i of the warp
+// reads lane 32 (warp mod 4) + i); valid after tmem_wait_ld().
+#define FQ_R8(r, i) "=r"((r)[i]), "=r"((r)[i + 1]), "=r"((r)[i + 2]), "=r"((r)[i + 3]), \
+                    "=r"((r)[i + 4]), "=r"((r)[i + 5]), "=r"((r)[i + 6]), "=r"((r)[i + 7])
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r)
 {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : FQ_R8(r, 0), FQ_R8(r, 8), FQ_R8(r, 16), FQ_R8(r, 24)
+        : "r"(addr));
+}
+#undef FQ_R8
+
+// Waits for the warp's TMEM loads.  Their registers may be used after it only,
+// by volatile statements, which stay behind it (passing 32 registers through
+// the wait instead costs as many moves).
+__device__ __forceinline__ void tmem_wait_ld()
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Registers a thread of the warpgroup may use from here on (the block keeps
+// the registers it was launched with: the shares add up to them).
+template <int kRegs>
+__device__ __forceinline__ void regs_up()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_down()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 // Packed pairs of FP32 (lower half first).
@@ -121,17 +281,26 @@ __device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi)
 {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+// acc += {lo, hi} * s, a pair of FMAs.
+__device__ __forceinline__ void fma2(uint64_t &acc, uint32_t lo, uint32_t hi, uint64_t s)
 {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
+    asm volatile("{\n\t.reg .b64 v;\n\t"
+                 "mov.b64 v, {%1, %2};\n\t"
+                 "fma.rn.f32x2 %0, v, %3, %0;\n\t}"
+                 : "+l"(acc)
+                 : "r"(lo), "r"(hi), "l"(s));
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+// acc += ({lo, hi} * {c0, c1}) * s.
+__device__ __forceinline__ void mul_fma2(uint64_t &acc, uint32_t lo, uint32_t hi, uint32_t c0,
+                                         uint32_t c1, uint64_t s)
 {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
+    asm volatile("{\n\t.reg .b64 v, c;\n\t"
+                 "mov.b64 v, {%1, %2};\n\t"
+                 "mov.b64 c, {%3, %4};\n\t"
+                 "mul.rn.f32x2 v, v, c;\n\t"
+                 "fma.rn.f32x2 %0, v, %5, %0;\n\t}"
+                 : "+l"(acc)
+                 : "r"(lo), "r"(hi), "r"(c0), "r"(c1), "l"(s));
 }
 
 // Two FP32 -> packed BF16 (round to nearest even, lo in the low half).
