@@ -108,17 +108,18 @@ def abi() -> ctypes.CDLL:
 
 
 def _call(name: str, *args) -> None:
-    status = getattr(abi(), name)(*args)
+    status = getattr(_lib or abi(), name)(*args)
     if status != 0:
         raise FQError(name, status)
 
 
-def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+def _stream() -> int:
+    # the current stream's handle without a Stream object (0.1 instead of 2.9 us)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
-def _p(t: torch.Tensor | None):
-    return ctypes.c_void_p(0 if t is None else t.data_ptr())
+def _p(t: torch.Tensor | None) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _need(t: torch.Tensor, dtype, name: str, ndim: int | None = None,
@@ -133,7 +134,7 @@ def _need(t: torch.Tensor, dtype, name: str, ndim: int | None = None,
         raise ValueError(f"{name} must be contiguous")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
@@ -142,12 +143,14 @@ def _need(t: torch.Tensor, dtype, name: str, ndim: int | None = None,
 def _on_device(**tensors):
     """Every tensor given is a CUDA tensor on the current device (the library
     launches there); None entries are skipped."""
-    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
+    cur = None
     for name, t in tensors.items():
         if t is None:
             continue
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
+        if cur is None:
+            cur = torch.cuda.current_device()
         if t.device.index != cur:
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
 

@@ -646,6 +646,329 @@ fq_status launch_matmul(const uint8_t *a, int64_t a_rows, const uint8_t *b, int6
     return launch_status();
 }
 
+// ---------------------------------------------------------------- few rows
+
+// The product for few rows per group (a decode step): the weights are read once
+// and bound the time, so the roles are swapped.  The 128 rows of the MMA are
+// weight rows (columns of c), its columns kT rows of a, and what is in flight is
+// weights: 2 CTAs per SM with 4 to 6 stages of 16 KB of them.  A lane of the
+// accumulator is a column of c; a block's products are scaled by the row's scale,
+// which a shuffle hands round.  With few tiles the blocks of K are split over a
+// cluster of S CTAs, whose sums are added through shared memory in rank order.
+template <int kT>
+struct Few {
+    static constexpr int stages = kT == 16 ? 6 : (kT == 32 ? 5 : 4);
+    static constexpr int w_bytes = 128 * kBlockK, x_bytes = kT * kBlockK;
+    static constexpr int tmem_cols = 128, bufs = tmem_cols / kT;
+    static constexpr int threads = 6 * 32;
+};
+
+template <int kT>
+struct FewTail {
+    uint64_t full[Few<kT>::stages], empty[Few<kT>::stages];
+    uint64_t acc_full[Few<kT>::bufs], acc_empty[Few<kT>::bufs];
+    uint32_t tmem;
+    int32_t abort;
+    // int32 off[G + 2], first[G + 2] follow
+};
+
+// Warps 0-3 add up the blocks, warp 4 issues the tensor copies, warp 5 the MMAs.
+template <int kT, Mode kMode, bool kF32>
+__global__ void __launch_bounds__(Few<kT>::threads, 2)
+    fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw,
+                          const MmArgs p, const int32_t S)
+{
+    using F = Few<kT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *sW = smem, *sX = sW + F::stages * F::w_bytes;
+    FewTail<kT> &t = *reinterpret_cast<FewTail<kT> *>(sX + F::stages * F::x_bytes);
+    int32_t *off = reinterpret_cast<int32_t *>(&t + 1), *first = off + p.G + 2;
+    volatile int32_t *abort = &t.abort;
+    const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t rank = S > 1 ? static_cast<int32_t>(cluster_rank()) : 0;
+
+    if (wid == 5) {
+        if (lane == 0) {
+            for (int i = 0; i < F::stages; i++) {
+                mbar_init(&t.full[i], 1);
+                mbar_init(&t.empty[i], 1);
+            }
+            for (int i = 0; i < F::bufs; i++) {
+                mbar_init(&t.acc_full[i], 1);
+                mbar_init(&t.acc_empty[i], 4);
+            }
+            t.abort = 0;
+            mbar_init_fence();
+        }
+        __syncwarp();
+        tmem_alloc<1>(&t.tmem, F::tmem_cols);
+    }
+    griddep_wait();  // the previous kernel's outputs (PDL launch)
+    if (wid == 0) {
+        const bool bad = load_row_groups(p.offs, p.G, p.M, kT, off, first);
+        if (bad && p.dev_status && blockIdx.x == 0 && lane == 0)
+            atomicOr(p.dev_status, 1);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = t.tmem;
+    // row tiles of all groups run fastest: tiles in flight share weights
+    const int32_t mt = first[p.G + 1], nt = (p.N + 127) / 128, ntiles = mt * nt;
+    const int32_t b_lo = static_cast<int32_t>(static_cast<int64_t>(p.KB) * rank / S);
+    const int32_t b_hi = static_cast<int32_t>(static_cast<int64_t>(p.KB) * (rank + 1) / S);
+    const int32_t idx0 = blockIdx.x / S, step = gridDim.x / S;
+
+    if (wid == 4) {
+        uint32_t s = 0, ph = 1;
+        for (int32_t idx = idx0; idx < ntiles && !*abort; idx += step) {
+            const int32_t j = idx / mt, i = idx - j * mt;
+            const int g = group_of_tile(first, p.G + 1, i);
+            if (g == p.G)
+                continue;
+            const int32_t row = off[g] + (i - first[g]) * kT, wrow = g * p.N + j * 128;
+            for (int32_t b = b_lo; b < b_hi; b++) {
+                warp_wait(smem_u32(&t.empty[s]), ph, abort);
+                if (*abort)
+                    break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&t.full[s], F::w_bytes + F::x_bytes);
+                    tma_load_2d(sW + s * F::w_bytes, &tw, b * kBlockK, wrow, &t.full[s]);
+                    tma_load_2d(sX + s * F::x_bytes, &tx, b * kBlockK, row, &t.full[s]);
+                }
+                if (++s == F::stages) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        if (*abort) {  // no copy may land after the CTA is gone: a millisecond is plenty
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 1000000)
+                ;
+        }
+    } else if (wid == 5) {
+        constexpr uint32_t idesc = idesc_e4m3(128, kT);
+        const uint64_t dw0 = smem_desc_sw128(sW), dx0 = smem_desc_sw128(sX);
+        uint32_t s = 0, ph = 0, it = 0;
+        for (int32_t idx = idx0; idx < ntiles && !*abort; idx += step) {
+            if (group_of_tile(first, p.G + 1, idx % mt) == p.G)
+                continue;
+            for (int32_t b = b_lo; b < b_hi; b++, it++) {
+                const uint32_t buf = it % F::bufs, bph = (it / F::bufs) & 1;
+                warp_wait(smem_u32(&t.full[s]), ph, abort);
+                warp_wait(smem_u32(&t.acc_empty[buf]), bph ^ 1, abort);
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t dw = dw0 + s * (F::w_bytes >> 4), dx = dx0 + s * (F::x_bytes >> 4);
+#pragma unroll
+                    for (int k = 0; k < kBlockK / 32; k++)
+                        mma_e4m3<1>(tmem + buf * kT, dw + 2 * k, dx + 2 * k, idesc, k > 0);
+                    mma_commit<1>(smem_u32(&t.acc_full[buf]));
+                    mma_commit<1>(smem_u32(&t.empty[s]));
+                }
+                if (++s == F::stages) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        if (*abort) {  // no MMA may be in flight when TMEM is freed
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 1000000)
+                ;
+        }
+    } else {
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * wid) << 16);
+        constexpr int kHold = (kT + 31) / 32;  // rows' scales of a lane
+        uint32_t it = 0;
+        for (int32_t idx = idx0; idx < ntiles && !*abort; idx += step) {
+            const int32_t j = idx / mt, i = idx - j * mt;
+            const int g = group_of_tile(first, p.G + 1, i);
+            const int32_t row0 = off[g] + (i - first[g]) * kT;
+            const int32_t rows = min(kT, off[g + 1] - row0);
+            const int32_t n = j * 128 + 32 * wid + lane;
+            float acc[kT];
+#pragma unroll
+            for (int e = 0; e < kT; e++)
+                acc[e] = 0.0f;
+            if (g < p.G) {
+                const float *sa[kHold];
+                float a[kHold], an[kHold];
+#pragma unroll
+                for (int h = 0; h < kHold; h++) {
+                    sa[h] = p.sa + static_cast<int64_t>(
+                                       min(row0 + min(lane + 32 * h, kT - 1), p.M - 1)) * p.KB;
+                    a[h] = b_lo < b_hi ? __ldg(sa[h] + b_lo) : 0.0f;
+                    an[h] = b_lo + 1 < b_hi ? __ldg(sa[h] + b_lo + 1) : 0.0f;
+                }
+                const float *sb = p.sb + (static_cast<int64_t>(g) * p.sb_rows +
+                                          (kMode == kRowScale ? min(n, p.N - 1) : j)) * p.KB;
+                float w = b_lo < b_hi ? __ldg(sb + b_lo) : 0.0f;
+                float wn = b_lo + 1 < b_hi ? __ldg(sb + b_lo + 1) : 0.0f;
+                for (int32_t b = b_lo; b < b_hi; b++, it++) {
+                    const uint32_t buf = it % F::bufs, bph = (it / F::bufs) & 1;
+                    float sc[kHold];
+#pragma unroll
+                    for (int h = 0; h < kHold; h++) {
+                        sc[h] = kMode == kRowScale ? a[h] : a[h] * w;
+                        a[h] = an[h];
+                        if (b + 2 < b_hi)
+                            an[h] = __ldg(sa[h] + b + 2);
+                    }
+                    const float wk = w;
+                    w = wn;
+                    if (b + 2 < b_hi)
+                        wn = __ldg(sb + b + 2);
+                    warp_wait(smem_u32(&t.acc_full[buf]), bph, abort);
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < kT / 16; c++) {
+                        uint32_t r[16];
+                        tmem_ld16(lanes + buf * kT + 16 * c, r);
+                        tmem_wait_ld16(r);
+                        if (c + 1 == kT / 16) {  // the buffer has been read
+                            tc_fence_before();
+                            mbar_arrive_cluster(smem_u32(&t.acc_empty[buf]), lane == 0);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; e++) {
+                            const int col = 16 * c + e;
+                            float v = __uint_as_float(r[e]);
+                            if (kMode == kRowScale)
+                                v *= wk;
+                            acc[col] = __fmaf_rn(v, __shfl_sync(0xffffffffu, sc[col / 32], col % 32),
+                                                 acc[col]);
+                        }
+                    }
+                }
+            }
+            if (S == 1) {
+                if (n < p.N && *abort == 0) {
+#pragma unroll
+                    for (int e = 0; e < kT; e++)
+                        if (e < rows) {
+                            const int64_t at = static_cast<int64_t>(row0 + e) * p.N + n;
+                            if (kF32)
+                                static_cast<float *>(p.c)[at] = acc[e];
+                            else
+                                static_cast<uint16_t *>(p.c)[at] =
+                                    static_cast<uint16_t>(cvt_bf16x2(acc[e], 0.0f));
+                        }
+                }
+            } else {  // one tile: its stages are free, every copy has been waited for
+                float *part = reinterpret_cast<float *>(smem);
+#pragma unroll
+                for (int e = 0; e < kT; e++)
+                    part[e * 128 + 32 * wid + lane] = acc[e];
+            }
+        }
+    }
+    if (S > 1) {
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        // CTA r adds up rows r, r + S, .. of the tile
+        if (wid < 4 && idx0 < ntiles && *abort == 0) {
+            const int32_t j = idx0 / mt, i = idx0 - j * mt;
+            const int g = group_of_tile(first, p.G + 1, i);
+            const int32_t row0 = off[g] + (i - first[g]) * kT;
+            const int32_t rows = min(kT, off[g + 1] - row0);
+            const int32_t n = j * 128 + 32 * wid + lane;
+            for (int32_t e = rank; e < rows; e += S) {
+                float v = 0.0f;
+                const float *own = reinterpret_cast<const float *>(smem) + e * 128 + 32 * wid + lane;
+                for (int32_t r = 0; r < S; r++)
+                    v += ld_cluster_f32(cluster_addr(own, r));
+                if (n < p.N) {
+                    const int64_t at = static_cast<int64_t>(row0 + e) * p.N + n;
+                    if (kF32)
+                        static_cast<float *>(p.c)[at] = v;
+                    else
+                        static_cast<uint16_t *>(p.c)[at] = static_cast<uint16_t>(cvt_bf16x2(v, 0.0f));
+                }
+            }
+        }
+        cluster_arrive();
+        cluster_wait();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (wid == 5)
+        tmem_free<1>(tmem, F::tmem_cols);
+    if (threadIdx.x == 0 && t.abort && p.dev_status)
+        atomicOr(p.dev_status, 2);
+}
+
+template <int kT, Mode kMode, bool kF32>
+fq_status launch_few(const uint8_t *a, const uint8_t *b, int64_t K, const MmArgs &p, cudaStream_t st)
+{
+    using F = Few<kT>;
+    CUtensorMap tx, tw;
+    if (!encode_tensor_map_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, a, K, p.M, K, kBlockK, kT,
+                              CU_TENSOR_MAP_SWIZZLE_128B, true) ||
+        !encode_tensor_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, b, K,
+                              static_cast<uint64_t>(p.G) * p.N, K, kBlockK, 128,
+                              CU_TENSOR_MAP_SWIZZLE_128B, true)) {
+        set_last_cuda_error(static_cast<int>(cudaErrorNotSupported));
+        return FQ_ERR_CUDA;
+    }
+    const auto kern = fp8_matmul_few_kernel<kT, kMode, kF32>;
+    const size_t dyn = 1024 + F::stages * (F::w_bytes + F::x_bytes) + sizeof(FewTail<kT>) +
+                       2 * (p.G + 2) * sizeof(int32_t);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(dyn)) != cudaSuccess)
+        return launch_status();
+    const int64_t nt = (p.N + 127) / 128;
+    // with one group the tiles are known, otherwise at most so many
+    const int64_t tiles = (p.offs ? p.M / kT + (p.G < p.M ? p.G : p.M) + 1 : (p.M + kT - 1) / kT) * nt;
+    // The split that leaves the SMs the least work each (the smallest of equals):
+    // 112 tiles on 152 SMs take one tile's time unsplit, 3/4 of it in quarters.
+    const int64_t sms = sm_count();
+    int S = 1;
+    int64_t best = (tiles + sms - 1) / sms * 8;
+    for (int s = 2; s <= 8 && tiles < sms && 2 * s <= p.KB; s *= 2) {
+        const int64_t cost = (tiles * s + sms - 1) / sms * 8 / s;
+        if (cost < best) {
+            best = cost;
+            S = s;
+        }
+    }
+    const int64_t most = S > 1 ? tiles : 2 * sms;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(S * (tiles < most ? tiles : most)));
+    cfg.blockDim = dim3(F::threads);
+    cfg.dynamicSmemBytes = dyn;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = S;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kern, tx, tw, p, static_cast<int32_t>(S)) != cudaSuccess)
+        return launch_status();
+    return launch_status();
+}
+
+template <Mode kMode, bool kF32>
+fq_status launch_forward(const uint8_t *a, const uint8_t *b, int64_t K, const MmArgs &p,
+                         cudaStream_t st)
+{
+    const int64_t mean = (static_cast<int64_t>(p.M) + p.G - 1) / p.G;  // rows of a group
+    if (mean <= 16)
+        return launch_few<16, kMode, kF32>(a, b, K, p, st);
+    if (mean <= 32)
+        return launch_few<32, kMode, kF32>(a, b, K, p, st);
+    if (mean <= 64)
+        return launch_few<64, kMode, kF32>(a, b, K, p, st);
+    return launch_matmul<2, kMode, kF32>(a, p.M, b, static_cast<int64_t>(p.G) * p.N, K, p.M, p, st);
+}
+
 // The transposed operands (rows of M tokens) re-laid for the weight gradient:
 // row r of the workspace holds the row's 128-token blocks, each at a multiple
 // of 128 bytes and filled up with zeros.  The rows of M tokens start at any
@@ -751,10 +1074,10 @@ extern "C" fq_status fp8_matmul(const uint8_t *a, const float *sa, int64_t M, in
     p.sb_rows = b_block == 1 ? p.N : (p.N + 127) / 128;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (b_block == 1)
-        return c_f32 ? launch_matmul<2, kRowScale, true>(a, M, b, G * N, K, M, p, st)
-                     : launch_matmul<2, kRowScale, false>(a, M, b, G * N, K, M, p, st);
-    return c_f32 ? launch_matmul<2, kTileScale, true>(a, M, b, G * N, K, M, p, st)
-                 : launch_matmul<2, kTileScale, false>(a, M, b, G * N, K, M, p, st);
+        return c_f32 ? launch_forward<kRowScale, true>(a, b, K, p, st)
+                     : launch_forward<kRowScale, false>(a, b, K, p, st);
+    return c_f32 ? launch_forward<kTileScale, true>(a, b, K, p, st)
+                 : launch_forward<kTileScale, false>(a, b, K, p, st);
 }
 
 extern "C" int64_t fp8_matmul_wgrad_workspace(int64_t M, int64_t N, int64_t K, int32_t G)

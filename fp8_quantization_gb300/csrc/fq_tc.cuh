@@ -177,6 +177,14 @@ __device__ __forceinline__ uint32_t cluster_addr(const void *own, uint32_t rank)
     return a;
 }
 
+// FP32 of the cluster's shared memory (address by cluster_addr).
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 // An arrival by the lanes with `pred`, on a barrier of this CTA or its pair's
 // (released to the CTA only: a cluster-wide release costs the length of a block,
 // and what it would order, the TMEM reads, has its own fences).
@@ -247,6 +255,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r)
         : FQ_R8(r, 0), FQ_R8(r, 8), FQ_R8(r, 16), FQ_R8(r, 24)
         : "r"(addr));
 }
+// 16 columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : FQ_R8(r, 0), FQ_R8(r, 8)
+        : "r"(addr));
+}
 #undef FQ_R8
 
 // Waits for the warp's TMEM loads.  Their registers may be used after it only,
@@ -268,6 +285,16 @@ template <int kRegs>
 __device__ __forceinline__ void regs_down()
 {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// The same where plain C++ uses the registers: they pass through the wait, so
+// that no use of them is moved ahead of it.
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t *r)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
 // Packed pairs of FP32 (lower half first).
