@@ -41,7 +41,7 @@ __device__ __forceinline__ uint32_t cvt_e4m3_pair(float lo, float hi)
 // memory, and 8 codes of one feature as one 8-byte shared store (the
 // conversion takes two tokens of a feature at a time, so nothing is
 // transposed in registers).  Rows of the transposed tile start at any byte of
-// yT: they are written as aligned 4-byte words, the bytes at both ends alone.
+// yT: they are written as aligned 16-byte pieces, the bytes at both ends alone.
 __global__ void __launch_bounds__(kThreads) fp8_quantize_cols_kernel(
     const uint16_t *__restrict__ x, int32_t M, int32_t K, const int64_t *__restrict__ offs,
     int32_t G, uint8_t *__restrict__ yT, float *__restrict__ scale, int64_t cap, int32_t *dev_status)
@@ -113,7 +113,9 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_cols_kernel(
             const uint32_t bits = (e & 1) ? m[e >> 1] >> 16 : m[e >> 1] & 0xFFFFu;
             const float amax = __uint_as_float(bits << 16);
             const bool special = bits >= 0x7F80u;
-            const float r = fminf(__fdiv_rn(448.0f, amax), FLT_MAX);
+            // a NaN factor gives every code 0x7F
+            const float r = special ? __uint_as_float(0x7FC00000u)
+                                    : fminf(__fdiv_rn(448.0f, amax), FLT_MAX);
             sc[e] = special ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, 448.0f);
             uint32_t w[2];
 #pragma unroll
@@ -127,8 +129,6 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_cols_kernel(
                 fmul2(p[0], p[1], r, p[0], p[1]);
                 fmul2(p[2], p[3], r, p[2], p[3]);
                 w[h] = cvt_e4m3_pair(p[0], p[1]) | (cvt_e4m3_pair(p[2], p[3]) << 16);
-                if (special)
-                    w[h] = 0x7F7F7F7Fu;
             }
             *reinterpret_cast<uint2 *>(tile + tile_byte(8 * c + e, 8 * q)) = make_uint2(w[0], w[1]);
         }
@@ -138,20 +138,46 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_cols_kernel(
             d[1] = make_float4(sc[4], sc[5], sc[6], sc[7]);
         }
         __syncthreads();
-        // row f0 + r of yT: bytes t0 .. t0 + len - 1, a warp per row
-        for (int r = wid; r < kFeat && f0 + r < K; r += kThreads / 32) {
-            uint8_t *dst = yT + static_cast<int64_t>(f0 + r) * M + t0;
-            const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(dst) & 3u);
-            const uint8_t *src = tile + tile_byte(r, 0);
-            for (int i = 4 * lane - mis; i < len; i += 128) {  // word at token i
-                if (i >= 0 && i + 4 <= len) {
-                    const uint32_t *s4 = reinterpret_cast<const uint32_t *>(src + (i & ~3));
-                    const uint32_t w = (i & 3) ? __funnelshift_r(s4[0], s4[1], 8 * (i & 3)) : s4[0];
-                    *reinterpret_cast<uint32_t *>(dst + i) = w;
-                } else {
-                    for (int b = max(i, 0); b < min(i + 4, len); b++)
-                        dst[b] = src[b];
+        // row f0 + r of yT: bytes t0 .. t0 + len - 1.  A full block: eight lanes a
+        // row, lane c the 16-byte piece of yT that holds token 16 c, and two of the
+        // 16 bytes at the ends that are no whole piece.
+        if (len == kTok) {
+            const int sub = lane >> 3, c8 = lane & 7;
+            uint8_t *dst = yT + static_cast<int64_t>(f0 + 4 * wid + sub) * M + t0;
+            const int64_t step = static_cast<int64_t>(M) * (kThreads / 8);
+#pragma unroll
+            for (int i = 0; i < kFeat * 8 / kThreads; i++, dst += step) {
+                const int r = 4 * wid + sub + i * (kThreads / 8);
+                if (f0 + r >= K)
+                    break;
+                const uint8_t *src = tile + tile_byte(r, 0);
+                const int lead = (16 - static_cast<int>(reinterpret_cast<uintptr_t>(dst) & 15u)) & 15;
+                if (lead == 0) {
+                    const uint2 *s8 = reinterpret_cast<const uint2 *>(src + 16 * c8);
+                    *reinterpret_cast<uint4 *>(dst + 16 * c8) =
+                        make_uint4(s8[0].x, s8[0].y, s8[1].x, s8[1].y);
+                    continue;
                 }
+                if (c8 < 7) {
+                    const int at = lead + 16 * c8, sh = 8 * (at & 3);
+                    const uint32_t *s4 = reinterpret_cast<const uint32_t *>(src + (at & ~3));
+                    const uint32_t v0 = s4[0], v1 = s4[1], v2 = s4[2], v3 = s4[3], v4 = s4[4];
+                    *reinterpret_cast<uint4 *>(dst + at) =
+                        make_uint4(__funnelshift_r(v0, v1, sh), __funnelshift_r(v1, v2, sh),
+                                   __funnelshift_r(v2, v3, sh), __funnelshift_r(v3, v4, sh));
+                }
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const int e = c8 + 8 * h, at = e < lead ? e : kTok - 16 + e;
+                    dst[at] = src[at];
+                }
+            }
+        } else {
+            for (int r = wid; r < kFeat && f0 + r < K; r += kThreads / 32) {
+                uint8_t *dst = yT + static_cast<int64_t>(f0 + r) * M + t0;
+                const uint8_t *src = tile + tile_byte(r, 0);
+                for (int i = lane; i < len; i += 32)
+                    dst[i] = src[i];
             }
         }
     }

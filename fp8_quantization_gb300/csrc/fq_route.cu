@@ -323,7 +323,8 @@ __device__ __forceinline__ uint32_t ld_cluster(const uint32_t *own, uint32_t ran
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortCluster = 8;
+constexpr int kSortCluster = 16;
+constexpr int kSortBatch = 8;  // loads in flight of a lane
 
 // Stable counting sort by one cluster.  Every warp owns a run of consecutive
 // pairs: it counts its pairs per expert in its own counters, the counters
@@ -348,10 +349,15 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_rows_kernel(
     uint32_t *mine = count + wid * E;
     const int64_t per = ((n + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
     const int64_t lo = min(n, per * (rank * kSortWarps + wid)), hi = min(n, lo + per);
-    for (int64_t i = lo + lane; i < hi; i += 32) {
-        const int32_t e = __ldg(ids + i);
-        if (e >= 0 && e < E)
-            atomicAdd(mine + e, 1u);
+    for (int64_t i0 = lo + lane; i0 < hi; i0 += 32 * kSortBatch) {
+        int32_t e[kSortBatch];
+#pragma unroll
+        for (int u = 0; u < kSortBatch; u++)
+            e[u] = i0 + 32 * u < hi ? __ldg(ids + i0 + 32 * u) : -1;
+#pragma unroll
+        for (int u = 0; u < kSortBatch; u++)
+            if (e[u] >= 0 && e[u] < E)
+                atomicAdd(mine + e[u], 1u);
     }
     __syncthreads();
     if (tid < E) {
@@ -401,23 +407,28 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_rows_kernel(
             count[w * E + tid] += start + before;
     }
     __syncthreads();
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-        const int64_t i = i0 + lane;
-        int32_t e = i < hi ? __ldg(ids + i) : -1;
-        if (e < 0 || e >= E)
-            e = -1;
-        const unsigned same = __match_any_sync(kFull, e);
-        int32_t row = -1;
-        if (e >= 0)
-            row = static_cast<int32_t>(mine[e] + __popc(same & ((1u << lane) - 1)));
-        __syncwarp();
-        if (e >= 0 && lane == __ffs(same) - 1)
-            mine[e] += __popc(same);
-        __syncwarp();
-        if (i < hi) {
-            row_of_pair[i] = row;
-            if (row >= 0)
-                pair_of_row[row] = static_cast<int32_t>(i);
+    for (int64_t i0 = lo + lane; i0 - lane < hi; i0 += 32 * kSortBatch) {
+        int32_t id[kSortBatch];
+#pragma unroll
+        for (int u = 0; u < kSortBatch; u++)
+            id[u] = i0 + 32 * u < hi ? __ldg(ids + i0 + 32 * u) : -1;
+#pragma unroll
+        for (int u = 0; u < kSortBatch; u++) {
+            const int64_t i = i0 + 32 * u;
+            const int32_t e = id[u] >= 0 && id[u] < E ? id[u] : -1;
+            const unsigned same = __match_any_sync(kFull, e);
+            int32_t row = -1;
+            if (e >= 0)
+                row = static_cast<int32_t>(mine[e] + __popc(same & ((1u << lane) - 1)));
+            __syncwarp();
+            if (e >= 0 && lane == __ffs(same) - 1)
+                mine[e] += __popc(same);
+            __syncwarp();
+            if (i < hi) {
+                row_of_pair[i] = row;
+                if (row >= 0)
+                    pair_of_row[row] = static_cast<int32_t>(i);
+            }
         }
     }
     // rows of no expert
@@ -539,10 +550,14 @@ extern "C" fq_status moe_sort_rows(const int32_t *ids, int64_t n, int32_t E, int
     if (cudaFuncSetAttribute(moe_sort_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(dyn)) != cudaSuccess)
         return launch_status();
-    // one CTA up to 4 pairs a thread
+    // one CTA up to 4 pairs a thread; 16 CTAs are beyond the portable cluster size
     unsigned ctas = 1;
     while (ctas < kSortCluster && n > static_cast<int64_t>(ctas) * 4 * kSortThreads)
         ctas *= 2;
+    if (ctas > 8 && cudaFuncSetAttribute(moe_sort_rows_kernel,
+                                         cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                        cudaSuccess)
+        return launch_status();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kSortThreads);
@@ -557,6 +572,15 @@ extern "C" fq_status moe_sort_rows(const int32_t *ids, int64_t n, int32_t E, int
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
+    if (ctas > 8) {
+        int fit = 0;
+        if (cudaOccupancyMaxActiveClusters(&fit, moe_sort_rows_kernel, &cfg) != cudaSuccess)
+            cudaGetLastError();
+        if (fit < 1) {
+            attr[1].val.clusterDim.x = 8;
+            cfg.gridDim = dim3(8);
+        }
+    }
     if (cudaLaunchKernelEx(&cfg, moe_sort_rows_kernel, ids, n, E, group_offsets, pair_of_row,
                            row_of_pair) != cudaSuccess)
         return launch_status();
