@@ -66,7 +66,8 @@ SIGNATURES = {
                          ctypes.c_float, _vp, _vp, _vp]),
     "moe_route_backward": (_int, [_vp, _int, _i64, _i32, _vp, _vp, _i32, _int, _int,
                                   ctypes.c_float, _vp, _vp]),
-    "moe_sort_rows": (_int, [_vp, _i64, _i32, _vp, _vp, _vp, _vp]),
+    "moe_sort_rows_workspace": (_i64, [_i64, _i32]),
+    "moe_sort_rows": (_int, [_vp, _i64, _i32, _vp, _vp, _vp, _vp, _i64, _vp]),
     "mxfp4_dequantize_rows": (_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
     "mxfp4_scales_mma_bytes": (_i64, [_i64, _i64]),
     "mxfp4_scales_mma_layout": (_int, [_vp, _i64, _i64, _vp, _vp]),
@@ -604,9 +605,15 @@ def moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.
     return dlogits
 
 
+def moe_sort_rows_workspace(n: int, n_experts: int) -> int:
+    """Bytes of workspace moe_sort_rows needs for n pairs (-1: rejected)."""
+    return int(abi().moe_sort_rows_workspace(int(n), int(n_experts)))
+
+
 def moe_sort_rows(ids: torch.Tensor, n_experts: int, group_offsets: torch.Tensor | None = None,
                   pair_of_row: torch.Tensor | None = None,
-                  row_of_pair: torch.Tensor | None = None):
+                  row_of_pair: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None):
     """Expert ids int32 (any shape, e.g. [T, k]) -> (group_offsets int64 [E+1],
     pair_of_row int32 [n], row_of_pair int32 shaped like ids): the (token,
     choice) pairs ordered by expert, and within an expert by index.  Row r
@@ -619,10 +626,17 @@ def moe_sort_rows(ids: torch.Tensor, n_experts: int, group_offsets: torch.Tensor
     _need(group_offsets, torch.int64, "group_offsets", numel=E + 1 if E > 0 else None)
     _need(pair_of_row, torch.int32, "pair_of_row", numel=n)
     _need(row_of_pair, torch.int32, "row_of_pair", numel=n)
+    need = moe_sort_rows_workspace(n, E)
+    if workspace is None and need > 0:
+        workspace = _empty((need,), torch.uint8, ids)
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace")
+        if workspace.numel() < need:
+            raise ValueError(f"workspace must hold {need} bytes, got {workspace.numel()}")
     _on_device(ids=ids, group_offsets=group_offsets, pair_of_row=pair_of_row,
-               row_of_pair=row_of_pair)
+               row_of_pair=row_of_pair, workspace=workspace)
     _call("moe_sort_rows", _p(ids), n, E, _p(group_offsets), _p(pair_of_row), _p(row_of_pair),
-          _stream())
+          _p(workspace), 0 if workspace is None else workspace.numel(), _stream())
     return group_offsets, pair_of_row, row_of_pair
 
 

@@ -705,6 +705,7 @@ __global__ void __launch_bounds__(Few<kT>::threads, 2)
         tmem_alloc<1>(&t.tmem, F::tmem_cols);
     }
     griddep_wait();  // the previous kernel's outputs (PDL launch)
+    griddep_launch_dependents();  // the next kernel may start its set-up
     if (wid == 0) {
         const bool bad = load_row_groups(p.offs, p.G, p.M, kT, off, first);
         if (bad && p.dev_status && blockIdx.x == 0 && lane == 0)
@@ -923,18 +924,12 @@ fq_status launch_few(const uint8_t *a, const uint8_t *b, int64_t K, const MmArgs
     const int64_t nt = (p.N + 127) / 128;
     // with one group the tiles are known, otherwise at most so many
     const int64_t tiles = (p.offs ? p.M / kT + (p.G < p.M ? p.G : p.M) + 1 : (p.M + kT - 1) / kT) * nt;
-    // The split that leaves the SMs the least work each (the smallest of equals):
-    // 112 tiles on 152 SMs take one tile's time unsplit, 3/4 of it in quarters.
+    // The blocks of K are split as far as all CTAs are still resident at once.
+    // (14336 x 4096 for one row, 112 tiles: quarters, 1.5 waves, took 19.5 us.)
     const int64_t sms = sm_count();
     int S = 1;
-    int64_t best = (tiles + sms - 1) / sms * 8;
-    for (int s = 2; s <= 8 && tiles < sms && 2 * s <= p.KB; s *= 2) {
-        const int64_t cost = (tiles * s + sms - 1) / sms * 8 / s;
-        if (cost < best) {
-            best = cost;
-            S = s;
-        }
-    }
+    while (S < 8 && tiles * S * 2 <= 2 * sms && 4 * S <= p.KB)
+        S *= 2;
     const int64_t most = S > 1 ? tiles : 2 * sms;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(S * (tiles < most ? tiles : most)));
@@ -973,7 +968,9 @@ fq_status launch_forward(const uint8_t *a, const uint8_t *b, int64_t K, const Mm
 // row r of the workspace holds the row's 128-token blocks, each at a multiple
 // of 128 bytes and filled up with zeros.  The rows of M tokens start at any
 // byte where M % 16 != 0, and the groups at any token: neither is a tensor
-// copy's alignment.  A lane makes 16 bytes from five aligned words.
+// copy's alignment.  A lane makes 16 bytes of kAlignRun consecutive blocks, each
+// from five aligned words.
+constexpr int kAlignRun = 4;
 __global__ void __launch_bounds__(kThreads) align_blocks_kernel(
     const uint8_t *__restrict__ a, int32_t a_rows, const uint8_t *__restrict__ b, int32_t b_rows,
     int32_t M, const int64_t *__restrict__ offs, int32_t G, int64_t pitch, uint8_t *__restrict__ out,
@@ -991,48 +988,72 @@ __global__ void __launch_bounds__(kThreads) align_blocks_kernel(
     griddep_launch_dependents();
     const int32_t blocks = first[G];
     const int64_t rows = static_cast<int64_t>(a_rows) + b_rows;
-    const int64_t quads = (rows + 3) / 4, items = quads * blocks;
+    const int32_t runs = (blocks + kAlignRun - 1) / kAlignRun;
+    const int64_t quads = (rows + 3) / 4, items = quads * runs;
     const int lane = threadIdx.x & 31, sub = lane >> 3, chunk = lane & 7;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
     for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
          w < items; w += step) {
-        const int64_t quad = w / blocks, r = 4 * quad + sub;
-        const int32_t blk = static_cast<int32_t>(w - quad * blocks);
+        const int64_t quad = w / runs, r = 4 * quad + sub;
+        const int32_t blk0 = static_cast<int32_t>(w - quad * runs) * kAlignRun;
         if (r >= rows)
             continue;
-        const int g = group_of_tile(first, G + 1, blk);
-        const int32_t t0 = off[g] + (blk - first[g]) * 128 + 16 * chunk;
-        const int32_t len = min(16, off[g + 1] - t0);
-        uint32_t o[4] = {0, 0, 0, 0};
-        if (len > 0) {
-            const bool in_a = r < a_rows;
-            const uint8_t *base = in_a ? a : b;
-            const int64_t size = static_cast<int64_t>(in_a ? a_rows : b_rows) * M;
-            const int64_t at = (in_a ? r : r - a_rows) * M + t0;
-            const int64_t w0 = at >> 2;
-            const int sh = 8 * static_cast<int>(at & 3);
-            uint32_t v[5];
+        const bool in_a = r < a_rows;
+        const uint8_t *base = in_a ? a : b;
+        const int64_t size = static_cast<int64_t>(in_a ? a_rows : b_rows) * M;
+        const int64_t row = (in_a ? r : r - a_rows) * M;
+        uint8_t *to = out + r * pitch + 16 * chunk;
+        int g = group_of_tile(first, G + 1, blk0);
+        uint32_t v[kAlignRun][5];
+        int32_t len[kAlignRun];
+        int64_t at[kAlignRun];
 #pragma unroll
-            for (int i = 0; i < 5; i++) {
-                v[i] = 0;
-                if (4 * (w0 + i) + 4 <= size) {
-                    v[i] = __ldg(reinterpret_cast<const uint32_t *>(base) + w0 + i);
-                } else {  // the tensor's last bytes
+        for (int u = 0; u < kAlignRun; u++) {
+            const int32_t blk = blk0 + u;
+            len[u] = 0;
+            if (blk >= blocks)
+                continue;
+            while (blk >= first[g + 1])
+                g++;
+            const int32_t t0 = off[g] + (blk - first[g]) * 128 + 16 * chunk;
+            len[u] = min(16, off[g + 1] - t0);
+            at[u] = row + t0;
+            const int64_t w0 = at[u] >> 2;
+            const uint32_t *from = reinterpret_cast<const uint32_t *>(base) + w0;
+            if (len[u] <= 0) {
+#pragma unroll
+                for (int i = 0; i < 5; i++)
+                    v[u][i] = 0;
+            } else if (4 * w0 + 20 <= size) {
+#pragma unroll
+                for (int i = 0; i < 5; i++)
+                    v[u][i] = __ldg(from + i);
+            } else {  // the tensor's last bytes
+#pragma unroll
+                for (int i = 0; i < 5; i++) {
+                    v[u][i] = 0;
                     for (int k = 0; k < 4; k++)
                         if (4 * (w0 + i) + k < size)
-                            v[i] |= static_cast<uint32_t>(base[4 * (w0 + i) + k]) << (8 * k);
+                            v[u][i] |= static_cast<uint32_t>(base[4 * (w0 + i) + k]) << (8 * k);
                 }
             }
+        }
+#pragma unroll
+        for (int u = 0; u < kAlignRun; u++) {
+            if (blk0 + u >= blocks)
+                break;
+            const int sh = 8 * static_cast<int>(at[u] & 3);
+            uint32_t o[4];
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                o[i] = __funnelshift_r(v[i], v[i + 1], sh);
-                const int keep = len - 4 * i;
+                o[i] = __funnelshift_r(v[u][i], v[u][i + 1], sh);
+                const int keep = len[u] - 4 * i;
                 if (keep < 4)
                     o[i] = keep > 0 ? o[i] & ((1u << (8 * keep)) - 1) : 0;
             }
+            *reinterpret_cast<uint4 *>(to + static_cast<int64_t>(blk0 + u) * 128) =
+                make_uint4(o[0], o[1], o[2], o[3]);
         }
-        *reinterpret_cast<uint4 *>(out + r * pitch + static_cast<int64_t>(blk) * 128 + 16 * chunk) =
-            make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -1117,7 +1138,7 @@ extern "C" fq_status fp8_matmul_wgrad(const uint8_t *aT, const float *aT_scale, 
     const int64_t blocks = fp4_to_fp8_cols_scale_capacity(M, G), pitch = 128 * blocks;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const size_t dyn = 2 * (G + 2) * sizeof(int32_t);
-    const int64_t warps = ((N + K + 3) / 4) * blocks;
+    const int64_t warps = ((N + K + 3) / 4) * ((blocks + kAlignRun - 1) / kAlignRun);
     const int grid = persistent_grid(align_blocks_kernel, kThreads, dyn, (warps + 7) / 8);
     if (launch_pdl(align_blocks_kernel, dim3(grid), dim3(kThreads), dyn, st, aT,
                    static_cast<int32_t>(N), bT, static_cast<int32_t>(K), static_cast<int32_t>(M),

@@ -16,7 +16,7 @@
 #include <cfloat>
 #include <cmath>
 
-#include "fq_tc.cuh"
+#include "fq_common.cuh"
 
 namespace fq {
 
@@ -313,43 +313,36 @@ __global__ void __launch_bounds__(kThreads) moe_route_backward_kernel(const Rout
 
 // ---------------------------------------------------------------- rows by expert
 
-// A 32-bit word of another CTA's shared memory, by the address of one's own.
-__device__ __forceinline__ uint32_t ld_cluster(const uint32_t *own, uint32_t rank)
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortBatch = 8;       // loads in flight of a lane
+constexpr int64_t kSortAlone = 8192;  // pairs that one CTA sorts by itself
+constexpr int64_t kSortMin = 4096;    // pairs of a CTA otherwise, at least
+
+// CTAs of the sort: the counters that each of them reads (one per expert and CTA)
+// stay within 64 Ki words.
+inline int32_t sort_ctas(int64_t n, int32_t E)
 {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(own, rank)) : "memory");
-    return v;
+    if (n <= kSortAlone)
+        return 1;
+    const int64_t by_pairs = (n + kSortMin - 1) / kSortMin, by_words = 65536 / E;
+    const int64_t most = by_words < 256 ? by_words : 256;
+    return static_cast<int32_t>(by_pairs < most ? by_pairs : most);
 }
 
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortCluster = 16;
-constexpr int kSortBatch = 8;  // loads in flight of a lane
-
-// Stable counting sort by one cluster.  Every warp owns a run of consecutive
-// pairs: it counts its pairs per expert in its own counters, the counters
-// become start rows (over the experts, then the CTAs, then the warps), and
-// the warp goes over its run again in order, a pair's row being its expert's
-// counter plus its rank among the lanes with the same expert.
-__global__ void __launch_bounds__(kSortThreads) moe_sort_rows_kernel(
-    const int32_t *__restrict__ ids, int64_t n, int32_t E, int64_t *__restrict__ offs,
-    int32_t *__restrict__ pair_of_row, int32_t *__restrict__ row_of_pair)
+// Pairs lo .. hi - 1 of warp `w` of all warps: runs of consecutive pairs.
+__device__ __forceinline__ void sort_run(int64_t n, int64_t w, int64_t warps, int64_t &lo, int64_t &hi)
 {
-    extern __shared__ uint32_t smem[];
-    __shared__ uint32_t warp_tot[kSortWarps];
-    uint32_t *total = smem, *count = smem + E;  // [E], [kSortWarps][E]
-    const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
-    const uint32_t rank = cluster_rank(), ctas = cluster_size();
-    for (int i = tid; i < kSortWarps * E; i += kSortThreads)
-        count[i] = 0;
-    __syncthreads();
-    griddep_wait();  // the previous kernel's outputs (PDL launch)
-    griddep_launch_dependents();
+    const int64_t per = ((n + warps - 1) / warps + 31) / 32 * 32;
+    lo = min(n, per * w);
+    hi = min(n, lo + per);
+}
 
-    uint32_t *mine = count + wid * E;
-    const int64_t per = ((n + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
-    const int64_t lo = min(n, per * (rank * kSortWarps + wid)), hi = min(n, lo + per);
-    for (int64_t i0 = lo + lane; i0 < hi; i0 += 32 * kSortBatch) {
+// Adds the pairs of a run to the counters of their experts.
+__device__ __forceinline__ void sort_count(const int32_t *__restrict__ ids, int64_t lo, int64_t hi,
+                                           int32_t E, uint32_t *count)
+{
+    for (int64_t i0 = lo + (threadIdx.x & 31); i0 < hi; i0 += 32 * kSortBatch) {
         int32_t e[kSortBatch];
 #pragma unroll
         for (int u = 0; u < kSortBatch; u++)
@@ -357,56 +350,108 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_rows_kernel(
 #pragma unroll
         for (int u = 0; u < kSortBatch; u++)
             if (e[u] >= 0 && e[u] < E)
-                atomicAdd(mine + e[u], 1u);
+                atomicAdd(count + e[u], 1u);
     }
+}
+
+// Pairs per expert of each CTA of the sort, counts[CTA][E].
+__global__ void __launch_bounds__(kSortThreads) moe_sort_count_kernel(
+    const int32_t *__restrict__ ids, int64_t n, int32_t E, uint32_t *__restrict__ counts)
+{
+    extern __shared__ uint32_t count[];  // [E]
+    for (int i = threadIdx.x; i < E; i += kSortThreads)
+        count[i] = 0;
     __syncthreads();
-    if (tid < E) {
-        uint32_t run = 0;
-#pragma unroll 8
-        for (int w = 0; w < kSortWarps; w++) {
-            const uint32_t c = count[w * E + tid];
-            count[w * E + tid] = run;
-            run += c;
-        }
-        total[tid] = run;
-    }
-    cluster_arrive();
-    cluster_wait();
-    uint32_t before = 0, all = 0;  // pairs of expert tid: in the CTAs before this one, in all
-    if (tid < E)
-        for (uint32_t r = 0; r < ctas; r++) {
-            const uint32_t v = ld_cluster(total + tid, r);
-            before += r < rank ? v : 0;
-            all += v;
-        }
-    cluster_arrive();  // the last read of another CTA's memory
-    uint32_t incl = all;
+    griddep_wait();  // the previous kernel's outputs (PDL launch)
+    griddep_launch_dependents();
+    int64_t lo, hi;
+    sort_run(n, static_cast<int64_t>(blockIdx.x) * kSortWarps + (threadIdx.x >> 5),
+             static_cast<int64_t>(gridDim.x) * kSortWarps, lo, hi);
+    sort_count(ids, lo, hi, E, count);
+    __syncthreads();
+    for (int i = threadIdx.x; i < E; i += kSortThreads)
+        counts[static_cast<int64_t>(blockIdx.x) * E + i] = count[i];
+}
+
+// Stable counting sort.  Every warp owns a run of consecutive pairs: it counts its
+// pairs per expert in its own counters, the counters become start rows (over the
+// experts, then the CTAs, then the warps), and the warp goes over its run again in
+// order, a pair's row being its expert's counter plus its rank among the lanes
+// with the same expert.  counts: of every CTA (nullptr with one CTA).
+__global__ void __launch_bounds__(kSortThreads) moe_sort_rows_kernel(
+    const int32_t *__restrict__ ids, int64_t n, int32_t E, const uint32_t *__restrict__ counts,
+    int64_t *__restrict__ offs, int32_t *__restrict__ pair_of_row, int32_t *__restrict__ row_of_pair)
+{
+    extern __shared__ uint32_t count[];  // [kSortWarps][E]
+    __shared__ uint32_t warp_tot[kSortWarps];
+    const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+    for (int i = tid; i < kSortWarps * E; i += kSortThreads)
+        count[i] = 0;
+    __syncthreads();
+    griddep_wait();  // the previous kernel's outputs (PDL launch)
+    griddep_launch_dependents();
+
+    uint32_t *mine = count + wid * E;
+    int64_t lo, hi;
+    sort_run(n, static_cast<int64_t>(blockIdx.x) * kSortWarps + wid,
+             static_cast<int64_t>(gridDim.x) * kSortWarps, lo, hi);
+    sort_count(ids, lo, hi, E, mine);
+    __syncthreads();
+
+    uint32_t rows = 0;  // of the experts before this round's, in the end of all
+    for (int e0 = 0; e0 < E; e0 += kSortThreads) {
+        const int e = e0 + tid;
+        uint32_t before = 0, all = 0;  // the expert's pairs: of the CTAs before, of all
+        if (e < E) {
+            if (counts) {
+                const int ctas = gridDim.x, self = blockIdx.x;
+#pragma unroll 32
+                for (int c = 0; c < ctas; c++) {
+                    const uint32_t v = __ldg(counts + static_cast<int64_t>(c) * E + e);
+                    before += c < self ? v : 0;
+                    all += v;
+                }
+            }
+            uint32_t run = 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t u = __shfl_up_sync(kFull, incl, d);
-        if (lane >= d)
-            incl += u;
-    }
-    if (lane == 31)
-        warp_tot[wid] = incl;
-    __syncthreads();
-    uint32_t start = incl - all, rows = 0;
-    for (int w = 0; w < kSortWarps; w++) {
-        const uint32_t v = warp_tot[w];
-        start += w < wid ? v : 0;
-        rows += v;
-    }
-    if (tid < E) {
-        if (rank == 0) {
-            offs[tid] = start;
-            if (tid == E - 1)
-                offs[E] = rows;
+            for (int w = 0; w < kSortWarps; w++) {
+                const uint32_t c = count[w * E + e];
+                count[w * E + e] = run;
+                run += c;
+            }
+            if (!counts)
+                all = run;
         }
-#pragma unroll 8
-        for (int w = 0; w < kSortWarps; w++)
-            count[w * E + tid] += start + before;
+        uint32_t incl = all;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t u = __shfl_up_sync(kFull, incl, d);
+            if (lane >= d)
+                incl += u;
+        }
+        if (lane == 31)
+            warp_tot[wid] = incl;
+        __syncthreads();
+        uint32_t start = rows + incl - all;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; w++) {
+            const uint32_t v = warp_tot[w];
+            start += w < wid ? v : 0;
+            rows += v;
+        }
+        if (e < E) {
+            if (blockIdx.x == 0)
+                offs[e] = start;
+#pragma unroll
+            for (int w = 0; w < kSortWarps; w++)
+                count[w * E + e] += start + before;
+        }
+        __syncthreads();
     }
-    __syncthreads();
+    if (blockIdx.x == 0 && tid == 0)
+        offs[E] = rows;
+
+    const int bits = 32 - __clz(E);  // of an expert, or of E for none
     for (int64_t i0 = lo + lane; i0 - lane < hi; i0 += 32 * kSortBatch) {
         int32_t id[kSortBatch];
 #pragma unroll
@@ -415,13 +460,17 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_rows_kernel(
 #pragma unroll
         for (int u = 0; u < kSortBatch; u++) {
             const int64_t i = i0 + 32 * u;
-            const int32_t e = id[u] >= 0 && id[u] < E ? id[u] : -1;
-            const unsigned same = __match_any_sync(kFull, e);
+            const int32_t e = id[u] >= 0 && id[u] < E ? id[u] : E;
+            unsigned same = kFull;  // the lanes with this lane's expert
+            for (int b = 0; b < bits; b++) {
+                const unsigned v = __ballot_sync(kFull, (e >> b) & 1);
+                same &= (e >> b) & 1 ? v : ~v;
+            }
             int32_t row = -1;
-            if (e >= 0)
+            if (e < E)
                 row = static_cast<int32_t>(mine[e] + __popc(same & ((1u << lane) - 1)));
             __syncwarp();
-            if (e >= 0 && lane == __ffs(same) - 1)
+            if (e < E && lane == __ffs(same) - 1)
                 mine[e] += __popc(same);
             __syncwarp();
             if (i < hi) {
@@ -432,10 +481,9 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_rows_kernel(
         }
     }
     // rows of no expert
-    for (int64_t r = rows + static_cast<int64_t>(rank) * kSortThreads + tid; r < n;
-         r += static_cast<int64_t>(ctas) * kSortThreads)
+    for (int64_t r = rows + static_cast<int64_t>(blockIdx.x) * kSortThreads + tid; r < n;
+         r += static_cast<int64_t>(gridDim.x) * kSortThreads)
         pair_of_row[r] = -1;
-    cluster_wait();
 }
 
 template <int kVals>
@@ -533,56 +581,45 @@ extern "C" fq_status moe_route_backward(const void *logits, int logits_f32, int6
     return launch_status();
 }
 
+extern "C" int64_t moe_sort_rows_workspace(int64_t n, int32_t E)
+{
+    using namespace fq;
+    if (n < 0 || n > INT32_MAX - 512 || E < 1 || E > FQ_COLS_MAX_GROUPS)
+        return -1;
+    const int64_t ctas = sort_ctas(n, E);
+    return ctas > 1 ? ctas * E * static_cast<int64_t>(sizeof(uint32_t)) : 0;
+}
+
 extern "C" fq_status moe_sort_rows(const int32_t *ids, int64_t n, int32_t E, int64_t *group_offsets,
-                                   int32_t *pair_of_row, int32_t *row_of_pair, void *stream)
+                                   int32_t *pair_of_row, int32_t *row_of_pair, void *workspace,
+                                   int64_t workspace_bytes, void *stream)
 {
     using namespace fq;
     if (n < 0 || n > INT32_MAX - 512)
         return FQ_ERR_SHAPE;
     if (E < 1 || E > FQ_COLS_MAX_GROUPS)
         return FQ_ERR_ARG;
-    if (!group_offsets || (n > 0 && (!ids || !pair_of_row || !row_of_pair)))
+    const int64_t need = moe_sort_rows_workspace(n, E);
+    if (workspace_bytes < need)
+        return FQ_ERR_ARG;
+    if (!group_offsets || (n > 0 && (!ids || !pair_of_row || !row_of_pair)) || (need > 0 && !workspace))
         return FQ_ERR_NULL;
     if (!aligned16(ids) || !aligned16(group_offsets) || !aligned16(pair_of_row) ||
-        !aligned16(row_of_pair))
+        !aligned16(row_of_pair) || !aligned16(workspace))
         return FQ_ERR_ALIGN;
-    const size_t dyn = (kSortWarps + 1) * static_cast<size_t>(E) * sizeof(uint32_t);
-    if (cudaFuncSetAttribute(moe_sort_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int32_t ctas = sort_ctas(n, E);
+    uint32_t *counts = ctas > 1 ? static_cast<uint32_t *>(workspace) : nullptr;
+    if (counts && launch_pdl(moe_sort_count_kernel, dim3(ctas), dim3(kSortThreads), E * sizeof(uint32_t),
+                             st, ids, n, E, counts) != cudaSuccess)
+        return launch_status();
+    const size_t dyn = kSortWarps * static_cast<size_t>(E) * sizeof(uint32_t);
+    if (dyn > 48 * 1024 &&
+        cudaFuncSetAttribute(moe_sort_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(dyn)) != cudaSuccess)
         return launch_status();
-    // one CTA up to 4 pairs a thread; 16 CTAs are beyond the portable cluster size
-    unsigned ctas = 1;
-    while (ctas < kSortCluster && n > static_cast<int64_t>(ctas) * 4 * kSortThreads)
-        ctas *= 2;
-    if (ctas > 8 && cudaFuncSetAttribute(moe_sort_rows_kernel,
-                                         cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-                        cudaSuccess)
-        return launch_status();
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = dyn;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (ctas > 8) {
-        int fit = 0;
-        if (cudaOccupancyMaxActiveClusters(&fit, moe_sort_rows_kernel, &cfg) != cudaSuccess)
-            cudaGetLastError();
-        if (fit < 1) {
-            attr[1].val.clusterDim.x = 8;
-            cfg.gridDim = dim3(8);
-        }
-    }
-    if (cudaLaunchKernelEx(&cfg, moe_sort_rows_kernel, ids, n, E, group_offsets, pair_of_row,
-                           row_of_pair) != cudaSuccess)
+    if (launch_pdl(moe_sort_rows_kernel, dim3(ctas), dim3(kSortThreads), dyn, st, ids, n, E, counts,
+                   group_offsets, pair_of_row, row_of_pair) != cudaSuccess)
         return launch_status();
     return launch_status();
 }

@@ -344,10 +344,15 @@ fq_status moe_route_backward(const void *logits, int logits_f32, int64_t T, int3
  *   pair_of_row   : int32 [n] (output) the pair of each row, rows ordered by
  *                   expert and within an expert by pair; -1 from offsets[E] on
  *   row_of_pair   : int32 [n] (output) the inverse; -1 for a pair of no expert
- * Requires 1 <= E <= FQ_COLS_MAX_GROUPS, 0 <= n < 2^31 - 512.
+ *   workspace     : device memory of at least moe_sort_rows_workspace(n, E)
+ *                   bytes (0 for few pairs: NULL will do), overwritten
+ * Requires 1 <= E <= FQ_COLS_MAX_GROUPS, 0 <= n < 2^31 - 512
+ * (moe_sort_rows_workspace: -1 otherwise).  Enqueues one or two kernels.
  */
+int64_t moe_sort_rows_workspace(int64_t n, int32_t E);
 fq_status moe_sort_rows(const int32_t *ids, int64_t n, int32_t E, int64_t *group_offsets,
-                        int32_t *pair_of_row, int32_t *row_of_pair, void *stream);
+                        int32_t *pair_of_row, int32_t *row_of_pair, void *workspace,
+                        int64_t workspace_bytes, void *stream);
 
 /*
  * MXFP4 -> BF16 dequantization ([MoE-FP4] 2.1: an element's value is its
