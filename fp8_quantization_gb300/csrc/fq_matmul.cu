@@ -954,14 +954,25 @@ template <Mode kMode, bool kF32>
 fq_status launch_forward(const uint8_t *a, const uint8_t *b, int64_t K, const MmArgs &p,
                          cudaStream_t st)
 {
-    const int64_t mean = (static_cast<int64_t>(p.M) + p.G - 1) / p.G;  // rows of a group
+    // Which kernel, by the mean rows of a group and the tiles (N x K 4096 x 7168
+    // unless said otherwise; us):
+    //   rows 32: few rows 9.9, one CTA a tile 19.9, pairs 26.4
+    //   rows 64: 12.3 (K split eight ways), 19.9, 26.5; but 14336 x 4096, where it
+    //            is not split: 24.0, 14.4, 18.8; 32 groups of 64: 176, 167, 197
+    //   rows 512: one CTA 21.4, pairs 27.0 (128 and 32 tiles); rows 1024: 37.6, 28.2
+    //   32 groups of 128 rows: 175, 201; of 256: 288, 227
+    const int64_t mean = (static_cast<int64_t>(p.M) + p.G - 1) / p.G;
+    const int64_t sms = sm_count(), nt = (p.N + 127) / 128;
+    const int64_t b_rows = static_cast<int64_t>(p.G) * p.N;
     if (mean <= 16)
         return launch_few<16, kMode, kF32>(a, b, K, p, st);
     if (mean <= 32)
         return launch_few<32, kMode, kF32>(a, b, K, p, st);
-    if (mean <= 64)
+    if (mean <= 64 && 2 * nt * p.G <= sms)
         return launch_few<64, kMode, kF32>(a, b, K, p, st);
-    return launch_matmul<2, kMode, kF32>(a, p.M, b, static_cast<int64_t>(p.G) * p.N, K, p.M, p, st);
+    if (p.G > 1 ? mean <= 128 : (mean + 127) / 128 * nt <= sms)
+        return launch_matmul<1, kMode, kF32>(a, p.M, b, b_rows, K, p.M, p, st);
+    return launch_matmul<2, kMode, kF32>(a, p.M, b, b_rows, K, p.M, p, st);
 }
 
 // The transposed operands (rows of M tokens) re-laid for the weight gradient:
@@ -1156,6 +1167,9 @@ extern "C" fq_status fp8_matmul_wgrad(const uint8_t *aT, const float *aT_scale, 
     p.N = static_cast<int32_t>(K);
     p.add = accumulate;
     const uint8_t *wb = ws + N * pitch;
+    if (mt * nt * G <= sm_count())  // the smaller tiles fill more SMs
+        return c_f32 ? launch_matmul<1, kWgrad, true>(ws, N, wb, K, pitch, G * N, p, st)
+                     : launch_matmul<1, kWgrad, false>(ws, N, wb, K, pitch, G * N, p, st);
     return c_f32 ? launch_matmul<2, kWgrad, true>(ws, N, wb, K, pitch, G * N, p, st)
                  : launch_matmul<2, kWgrad, false>(ws, N, wb, K, pitch, G * N, p, st);
 }
