@@ -68,6 +68,9 @@ template <typename Kernel>
 inline int persistent_grid(Kernel kernel, int threads, size_t smem, int64_t work_ctas,
                            int waves = 1)
 {
+    // at most one CTA per SM: no need to ask how many fit
+    if (work_ctas <= sm_count())
+        return static_cast<int>(work_ctas < 1 ? 1 : work_ctas);
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) !=
             cudaSuccess ||

@@ -511,23 +511,34 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 tc_fence_after();
                 const uint64_t sc = pack2(__float_as_uint(s), __float_as_uint(s));
                 const uint32_t addr = lane_base + buf * kBufCols;
+                // kChunk columns at a time; with a scale per column, those of the
+                // chunk are fetched while it is on its way (16 columns: registers)
+                constexpr int kChunk = kColScale ? 16 : 32;
 #pragma unroll
-                for (int c = 0; c < kCols / 32; c++) {
-                    uint32_t r[32];
-                    tmem_ld32(addr + 32 * c, r);
+                for (int c = 0; c < kCols / kChunk; c++) {
+                    uint32_t r[kChunk];
+                    uint4 cs[kColScale ? 4 : 1];
+                    if (kColScale) {
+                        tmem_ld16(addr + kChunk * c, r);
+#pragma unroll
+                        for (int q = 0; q < 4; q++)
+                            cs[kColScale ? q : 0] =
+                                *reinterpret_cast<const uint4 *>(cols + kChunk * c + 4 * q);
+                    } else {
+                        tmem_ld32(addr + kChunk * c, r);
+                    }
                     tmem_wait_ld();
-                    if (c + 1 == kCols / 32) {  // the buffer has been read
+                    if (c + 1 == kCols / kChunk) {  // the buffer has been read
                         tc_fence_before();
                         mbar_arrive_cluster(read0 + 8 * buf, leader);
                     }
-                    uint64_t *o = acc + 16 * c;
+                    uint64_t *o = acc + kChunk / 2 * c;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
+                    for (int e = 0; e < kChunk; e += 4) {
                         if (kColScale) {
-                            const uint4 cs =
-                                *reinterpret_cast<const uint4 *>(cols + 32 * c + e);
-                            mul_fma2(o[e / 2], r[e], r[e + 1], cs.x, cs.y, sc);
-                            mul_fma2(o[e / 2 + 1], r[e + 2], r[e + 3], cs.z, cs.w, sc);
+                            const uint4 q = cs[kColScale ? e / 4 : 0];
+                            mul_fma2(o[e / 2], r[e], r[e + 1], q.x, q.y, sc);
+                            mul_fma2(o[e / 2 + 1], r[e + 2], r[e + 3], q.z, q.w, sc);
                         } else {
                             fma2(o[e / 2], r[e], r[e + 1], sc);
                             fma2(o[e / 2 + 1], r[e + 2], r[e + 3], sc);
