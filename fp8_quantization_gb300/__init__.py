@@ -538,17 +538,21 @@ def fp8_matmul_wgrad(aT: torch.Tensor, aT_scale: torch.Tensor, bT: torch.Tensor,
     out = _empty((G, N, K), dt, aT) if out is None else out
     _need(out, dt, "out", numel=G * N * K)
     need = fp8_matmul_wgrad_workspace(M, N, K, G)
-    workspace = _empty((max(need, 0),), torch.uint8, aT) if workspace is None else workspace
-    _need(workspace, torch.uint8, "workspace")
-    if workspace.numel() < need:
-        raise ValueError(f"workspace must hold {need} bytes, got {workspace.numel()}")
+    if group_offsets is None and M % 16 == 0 and M > 0:
+        need = 0  # read in place
+    if workspace is None and need > 0:
+        workspace = _empty((need,), torch.uint8, aT)
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace")
+        if workspace.numel() < need:
+            raise ValueError(f"workspace must hold {need} bytes, got {workspace.numel()}")
     _dev_status(dev_status)
     _on_device(aT=aT, aT_scale=aT_scale, bT=bT, bT_scale=bT_scale, group_offsets=group_offsets,
                out=out, workspace=workspace, dev_status=dev_status)
     _call("fp8_matmul_wgrad", _p(aT), _p(aT_scale), N, _p(bT), _p(bT_scale), K, M,
           _p(group_offsets), G, min(aT_scale.shape[0], bT_scale.shape[0]), _p(out),
-          int(dt == torch.float32), int(bool(accumulate)), _p(workspace), workspace.numel(),
-          _p(dev_status), _stream())
+          int(dt == torch.float32), int(bool(accumulate)), _p(workspace),
+          0 if workspace is None else workspace.numel(), _p(dev_status), _stream())
     return out
 
 

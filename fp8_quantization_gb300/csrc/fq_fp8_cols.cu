@@ -47,7 +47,8 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_cols_kernel(
     int32_t G, uint8_t *__restrict__ yT, float *__restrict__ scale, int64_t cap, int32_t *dev_status)
 {
     extern __shared__ int32_t dyn[];
-    __shared__ uint32_t red[kThreads / 32][kFeat / 2];
+    __shared__ __align__(16) uint16_t red[kThreads / 32][kFeat];
+    __shared__ __align__(16) float factor[kFeat];
     __shared__ __align__(16) uint8_t tile[kTileBytes];
     int32_t *off = dyn, *first = dyn + G + 2;
     const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
@@ -96,27 +97,28 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_cols_kernel(
         for (int i = 0; i < 4; i++)
             m[i] = max_u16x2(m[i], __shfl_xor_sync(0xffffffffu, m[i], 16));
         if (lane < 16)
-            *reinterpret_cast<uint4 *>(&red[wid][4 * c]) = make_uint4(m[0], m[1], m[2], m[3]);
+            *reinterpret_cast<uint4 *>(&red[wid][8 * c]) = make_uint4(m[0], m[1], m[2], m[3]);
         __syncthreads();  // also: the previous tile's rows are written out
+        if (tid < kFeat) {  // one thread a feature: the divisions are made once
+            uint32_t bits = 0;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; w++) {
-            const uint4 o = *reinterpret_cast<const uint4 *>(&red[w][4 * c]);
-            m[0] = max_u16x2(m[0], o.x);
-            m[1] = max_u16x2(m[1], o.y);
-            m[2] = max_u16x2(m[2], o.z);
-            m[3] = max_u16x2(m[3], o.w);
-        }
-        const uint32_t *vw = reinterpret_cast<const uint32_t *>(v);
-        float sc[8];
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const uint32_t bits = (e & 1) ? m[e >> 1] >> 16 : m[e >> 1] & 0xFFFFu;
-            const float amax = __uint_as_float(bits << 16);
+            for (int w = 0; w < kThreads / 32; w++)
+                bits = max(bits, static_cast<uint32_t>(red[w][tid]));
+            const float amax = __uint_as_float(bits << 16), nan = __uint_as_float(0x7FC00000u);
             const bool special = bits >= 0x7F80u;
             // a NaN factor gives every code 0x7F
-            const float r = special ? __uint_as_float(0x7FC00000u)
-                                    : fminf(__fdiv_rn(448.0f, amax), FLT_MAX);
-            sc[e] = special ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, 448.0f);
+            factor[tid] = special ? nan : fminf(__fdiv_rn(448.0f, amax), FLT_MAX);
+            if (g < G && f0 + tid < K)
+                scale[static_cast<int64_t>(blk) * K + f0 + tid] =
+                    special ? nan : __fdiv_rn(amax, 448.0f);
+        }
+        __syncthreads();
+        const uint32_t *vw = reinterpret_cast<const uint32_t *>(v);
+        float r8[8];
+        *reinterpret_cast<float4 *>(r8) = *reinterpret_cast<const float4 *>(factor + 8 * c);
+        *reinterpret_cast<float4 *>(r8 + 4) = *reinterpret_cast<const float4 *>(factor + 8 * c + 4);
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
             uint32_t w[2];
 #pragma unroll
             for (int h = 0; h < 2; h++) {
@@ -126,16 +128,11 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_cols_kernel(
                     const uint32_t u = vw[4 * (4 * h + j) + (e >> 1)];
                     p[j] = (e & 1) ? bf16_hi(u) : bf16_lo(u);
                 }
-                fmul2(p[0], p[1], r, p[0], p[1]);
-                fmul2(p[2], p[3], r, p[2], p[3]);
+                fmul2(p[0], p[1], r8[e], p[0], p[1]);
+                fmul2(p[2], p[3], r8[e], p[2], p[3]);
                 w[h] = cvt_e4m3_pair(p[0], p[1]) | (cvt_e4m3_pair(p[2], p[3]) << 16);
             }
             *reinterpret_cast<uint2 *>(tile + tile_byte(8 * c + e, 8 * q)) = make_uint2(w[0], w[1]);
-        }
-        if (q == 0 && g < G && f < K) {
-            float4 *d = reinterpret_cast<float4 *>(scale + static_cast<int64_t>(blk) * K + f);
-            d[0] = make_float4(sc[0], sc[1], sc[2], sc[3]);
-            d[1] = make_float4(sc[4], sc[5], sc[6], sc[7]);
         }
         __syncthreads();
         // row f0 + r of yT: bytes t0 .. t0 + len - 1.  A full block: eight lanes a

@@ -668,6 +668,8 @@ fq_status launch_matmul(const uint8_t *a, int64_t a_rows, const uint8_t *b, int6
 // cluster of S CTAs, whose sums are added through shared memory in rank order.
 template <int kT>
 struct Few {
+    // CTAs per SM and their stages: about 200 KB of weights in flight per SM
+    static constexpr int per_sm = 2;
     static constexpr int stages = kT == 16 ? 6 : (kT == 32 ? 5 : 4);
     static constexpr int w_bytes = 128 * kBlockK, x_bytes = kT * kBlockK;
     static constexpr int tmem_cols = 128, bufs = tmem_cols / kT;
@@ -685,7 +687,7 @@ struct FewTail {
 
 // Warps 0-3 add up the blocks, warp 4 issues the tensor copies, warp 5 the MMAs.
 template <int kT, Mode kMode, bool kF32>
-__global__ void __launch_bounds__(Few<kT>::threads, 2)
+__global__ void __launch_bounds__(Few<kT>::threads, Few<kT>::per_sm)
     fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw,
                           const MmArgs p, const int32_t S)
 {
@@ -935,13 +937,15 @@ fq_status launch_few(const uint8_t *a, const uint8_t *b, int64_t K, const MmArgs
     const int64_t nt = (p.N + 127) / 128;
     // with one group the tiles are known, otherwise at most so many
     const int64_t tiles = (p.offs ? p.M / kT + (p.G < p.M ? p.G : p.M) + 1 : (p.M + kT - 1) / kT) * nt;
-    // The blocks of K are split as far as all CTAs are still resident at once.
-    // (14336 x 4096 for one row, 112 tiles: quarters, 1.5 waves, took 19.5 us.)
+    // The blocks of K are split while an SM has no more than one CTA (with 64 rows,
+    // which keep a CTA longer, two): 112 tiles of 14336 x 4096 took 15 to 16 us for 1
+    // to 32 rows unsplit, 17 to 20 us halved, 20 us in quarters.
     const int64_t sms = sm_count();
     int S = 1;
-    while (S < 8 && tiles * S * 2 <= 2 * sms && 4 * S <= p.KB)
+    const int64_t slots = (kT == 64 ? 2 : 1) * sms;
+    while (S < 8 && tiles * S * 2 <= slots && 4 * S <= p.KB)
         S *= 2;
-    const int64_t most = S > 1 ? tiles : 2 * sms;
+    const int64_t most = S > 1 ? tiles : F::per_sm * sms;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(S * (tiles < most ? tiles : most)));
     cfg.blockDim = dim3(F::threads);
@@ -1149,23 +1153,33 @@ extern "C" fq_status fp8_matmul_wgrad(const uint8_t *aT, const float *aT_scale, 
     const int64_t mt = (N + 127) / 128, nt = (K + 127) / 128;
     if (need < 0 || mt > INT32_MAX / nt / G || N > INT32_MAX / G)  // 32-bit tiles and rows of c
         return FQ_ERR_SHAPE;
-    if (cap < fp4_to_fp8_cols_scale_capacity(M, G) || workspace_bytes < need)
+    // one group from token 0 on, rows of M tokens 16-byte aligned: the blocks lie
+    // where tensor copies can fetch them
+    const bool in_place = !group_offsets && M % 16 == 0 && M > 0;
+    if (cap < fp4_to_fp8_cols_scale_capacity(M, G) || (!in_place && workspace_bytes < need))
         return FQ_ERR_ARG;
-    if ((M > 0 && (!aT || !aT_scale || !bT || !bT_scale)) || !c || !workspace)
+    if ((M > 0 && (!aT || !aT_scale || !bT || !bT_scale)) || !c || (!in_place && !workspace))
         return FQ_ERR_NULL;
     if (!aligned16(aT) || !aligned16(aT_scale) || !aligned16(bT) || !aligned16(bT_scale) ||
         !aligned16(c) || !aligned16(workspace) || !aligned16(group_offsets))
         return FQ_ERR_ALIGN;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t blocks = fp4_to_fp8_cols_scale_capacity(M, G), pitch = 128 * blocks;
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const size_t dyn = 2 * (G + 2) * sizeof(int32_t);
-    const int64_t warps = ((N + K + 3) / 4) * ((blocks + kAlignRun - 1) / kAlignRun);
-    const int grid = persistent_grid(align_blocks_kernel, kThreads, dyn, (warps + 7) / 8);
-    if (launch_pdl(align_blocks_kernel, dim3(grid), dim3(kThreads), dyn, st, aT,
-                   static_cast<int32_t>(N), bT, static_cast<int32_t>(K), static_cast<int32_t>(M),
-                   group_offsets, G, pitch, ws, dev_status) != cudaSuccess)
-        return launch_status();
+    const uint8_t *wa = aT, *wb = bT;
+    int64_t pitch = M;
+    if (!in_place) {
+        const int64_t blocks = fp4_to_fp8_cols_scale_capacity(M, G);
+        pitch = 128 * blocks;
+        uint8_t *ws = static_cast<uint8_t *>(workspace);
+        wa = ws;
+        wb = ws + N * pitch;
+        const size_t dyn = 2 * (G + 2) * sizeof(int32_t);
+        const int64_t warps = ((N + K + 3) / 4) * ((blocks + kAlignRun - 1) / kAlignRun);
+        const int grid = persistent_grid(align_blocks_kernel, kThreads, dyn, (warps + 7) / 8);
+        if (launch_pdl(align_blocks_kernel, dim3(grid), dim3(kThreads), dyn, st, aT,
+                       static_cast<int32_t>(N), bT, static_cast<int32_t>(K), static_cast<int32_t>(M),
+                       group_offsets, G, pitch, ws, dev_status) != cudaSuccess)
+            return launch_status();
+    }
     MmArgs p = {};
     p.sa = aT_scale;
     p.sb = bT_scale;
@@ -1177,10 +1191,9 @@ extern "C" fq_status fp8_matmul_wgrad(const uint8_t *aT, const float *aT_scale, 
     p.R = static_cast<int32_t>(N);
     p.N = static_cast<int32_t>(K);
     p.add = accumulate;
-    const uint8_t *wb = ws + N * pitch;
     if (mt * nt * G <= sm_count())  // the smaller tiles fill more SMs
-        return c_f32 ? launch_matmul<1, kWgrad, true>(ws, N, wb, K, pitch, G * N, p, st)
-                     : launch_matmul<1, kWgrad, false>(ws, N, wb, K, pitch, G * N, p, st);
-    return c_f32 ? launch_matmul<2, kWgrad, true>(ws, N, wb, K, pitch, G * N, p, st)
-                 : launch_matmul<2, kWgrad, false>(ws, N, wb, K, pitch, G * N, p, st);
+        return c_f32 ? launch_matmul<1, kWgrad, true>(wa, N, wb, K, pitch, G * N, p, st)
+                     : launch_matmul<1, kWgrad, false>(wa, N, wb, K, pitch, G * N, p, st);
+    return c_f32 ? launch_matmul<2, kWgrad, true>(wa, N, wb, K, pitch, G * N, p, st)
+                 : launch_matmul<2, kWgrad, false>(wa, N, wb, K, pitch, G * N, p, st);
 }

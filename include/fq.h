@@ -281,13 +281,14 @@ fq_status fp8_quantize_cols(const void *x, int64_t M, int64_t K, const int64_t *
  * sums in binary32, rounded once.  An empty group's gradient is 0.
  * accumulate = 1 adds to what c holds instead (an empty group's stays).
  *   workspace : device memory of at least fp8_matmul_wgrad_workspace(M, N, K,
- *        G) bytes, 16-byte aligned, overwritten; the operands are re-laid there
- *        block by block (-1 for a rejected shape)
+ *        G) bytes (-1 for a rejected shape), 16-byte aligned, overwritten; the
+ *        operands are re-laid there block by block.  Not used, and may be NULL
+ *        and 0, where group_offsets is NULL and M % 16 == 0.
  *   dev_status : as in fp8_matmul
  * Requires N, K > 0 (K % 8 == 0 stores 16 bytes at a time), 1 <= G <=
  * FQ_COLS_MAX_GROUPS, 0 <= M, cap >= fp4_to_fp8_cols_scale_capacity(M, G),
- * 128 cap < 2^31 - 512.  Enqueues two kernels.  The same inputs give the same
- * bits.
+ * 128 cap < 2^31 - 512.  Enqueues one or two kernels.  The same inputs give the
+ * same bits.
  */
 int64_t fp8_matmul_wgrad_workspace(int64_t M, int64_t N, int64_t K, int32_t G);
 fq_status fp8_matmul_wgrad(const uint8_t *aT, const float *aT_scale, int64_t N, const uint8_t *bT,

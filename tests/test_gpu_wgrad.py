@@ -160,6 +160,17 @@ def test_wgrad(fq, case, N, K):
     assert int(status) == 0
 
 
+@pytest.mark.parametrize("M", [1, 16, 112, 128, 1000, 1008])
+def test_wgrad_of_one_group(fq, M):
+    """Without offsets; M % 16 == 0 reads the operands in place."""
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    offs, cap = np.array([0, M]), fq.fp4_to_fp8_cols_scale_capacity(M, 1)
+    a, sa = operands(M, 200, offs, gen, cap)
+    b, sb = operands(M, 264, offs, gen, cap)
+    ref, mag, blocks = reference(a, sa, b, sb, offs)
+    check(fq.fp8_matmul_wgrad(a, sa, b, sb), ref, mag, blocks)
+
+
 def test_a_nan_block_stays_in_its_group_and_row(fq):
     offs = np.array([0, 100, 210, 300])
     gen = torch.Generator(device="cuda").manual_seed(1)
