@@ -9,8 +9,10 @@
 //   r = min(448 / amax, FLT_MAX), s = amax / 448, code = E4M3(x * r);
 //   a block holding NaN or Inf gets s = NaN and codes 0x7F.
 //
-// Bound by HBM: 2 bytes read and 1 written per element, 4 bytes written per
-// block and feature.
+// 2 bytes read and 1 written per element, 4 bytes written per block and feature:
+// 65536 x 2048 in 85 us, 4.8 TB/s.  HBM and the instructions share the bound (issue
+// slots 60 % busy, 4 CTAs per SM).  Written as 4-byte words, a warp a row, it took
+// 172 us; with the divisions in every thread 94 us.
 #include <cfloat>
 
 #include "fq_tc.cuh"

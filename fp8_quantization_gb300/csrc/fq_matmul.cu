@@ -266,8 +266,23 @@ __device__ __forceinline__ float4 load_scales(const float *s, int64_t step, int3
 // accumulator.  Warps 0-7 add up the scaled blocks (warp w: TMEM lanes 32 (w mod
 // 4).., half w / 4 of the columns), warp 8 issues the tensor copies, warp 9 of
 // the cluster's first CTA the MMAs, warp 10 fetches the scales of the columns
-// where every column has its own.  Two TMEM buffers: the MMAs of block b + 1 run while block b is
-// scaled and added.
+// where every column has its own.  Two TMEM buffers: the MMAs of block b + 1 run
+// while block b is scaled and added.
+//
+// What bounds it.  A block of a 256 x 256 tile takes the tensor cores 512 cycles
+// and its operands 64 KB of shared-memory traffic per SM (512 cycles as well), but
+// the warps 0-7 about 820: the TMEM loads, 64 packed FMAs a thread (256 cycles for
+// the two warps of a scheduler) and about 20 more instructions a warp at their full
+// latency, which two warps a scheduler do not hide.  16384 x 4096 x 7168: 337 us
+// (2.86 PFLOP/s) with the L2 flushed, 375 us back to back at the lower clocks that
+// this draws; without scaling and adding the same loop takes 285 us.  With a scale
+// per column it is twice the FMAs and a shared load per four columns: 566 us.
+// Why so: pairs of CTAs halve the traffic of b (one CTA a tile: 415 us before the
+// rest); 256 accumulator columns need 128 registers a thread, so the other roles
+// give theirs up, down to 104 (at 56 they spill, and the kernel takes 10 to 20 %
+// longer); 16 columns less pressure but more waits a column (192-column tiles: 410
+// us); half-tile MMAs read a twice (500 us); 16 adding warps have too few registers
+// (414 us and more).
 template <int kCtas, Mode kMode, bool kF32>
 __global__ void __launch_bounds__(kMmThreads, 1)
     fp8_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
@@ -662,10 +677,14 @@ fq_status launch_matmul(const uint8_t *a, int64_t a_rows, const uint8_t *b, int6
 // The product for few rows per group (a decode step): the weights are read once
 // and bound the time, so the roles are swapped.  The 128 rows of the MMA are
 // weight rows (columns of c), its columns kT rows of a, and what is in flight is
-// weights: 2 CTAs per SM with 4 to 6 stages of 16 KB of them.  A lane of the
+// weights: 2 CTAs per SM with 4 to 6 stages of 16 KB of them (3 CTAs with 4 stages
+// were 8 % slower, 1 CTA with 11 stages 5 %).  A lane of the
 // accumulator is a column of c; a block's products are scaled by the row's scale,
 // which a shuffle hands round.  With few tiles the blocks of K are split over a
 // cluster of S CTAs, whose sums are added through shared memory in rank order.
+// Bound by HBM: 512 rows over 32 experts of 4096 x 7168 in 150 to 160 us, 5.9 to 6.3
+// TB/s; one row through 14336 x 4096 in 15.3 us, 3.8 TB/s, of which the launch, the
+// set-up and the first and last bytes' latency are about 6 us.
 template <int kT>
 struct Few {
     // CTAs per SM and their stages: about 200 KB of weights in flight per SM
@@ -995,7 +1014,9 @@ fq_status launch_forward(const uint8_t *a, const uint8_t *b, int64_t K, const Mm
 // of 128 bytes and filled up with zeros.  The rows of M tokens start at any
 // byte where M % 16 != 0, and the groups at any token: neither is a tensor
 // copy's alignment.  A lane makes 16 bytes of kAlignRun consecutive blocks, each
-// from five aligned words.
+// from five aligned words.  Bound by HBM (every byte read and written once): 65536
+// tokens x 9216 rows in 209 us, 6.0 TB/s; a block at a time, with a division and a
+// search each, took 325 us.
 constexpr int kAlignRun = 4;
 __global__ void __launch_bounds__(kThreads) align_blocks_kernel(
     const uint8_t *__restrict__ a, int32_t a_rows, const uint8_t *__restrict__ b, int32_t b_rows,

@@ -73,7 +73,10 @@ __device__ __forceinline__ uint32_t warp_best(uint32_t key, int idx, int &best)
     return m;
 }
 
-// One warp per token; lane l holds the experts l + 32 i.  kVals >= E / 32.
+// One warp per token; lane l holds the experts l + 32 i.  kVals >= E / 32.  A choice
+// is two warp reductions (the largest key, the lowest index that has it), so ties
+// need no sort.  Bound by those k rounds of dependent instructions, not by memory:
+// 16384 x 256 BF16 logits, k = 8, in 20 us (8.4 MB); 8 tokens with groups in 8 us.
 template <int kVals, bool kBf16, bool kSigmoid, bool kNorm>
 __global__ void __launch_bounds__(kThreads) moe_route_kernel(const RouteArgs p)
 {
@@ -233,7 +236,8 @@ __device__ __forceinline__ void store_grad(void *dl, int64_t at, float v, bool b
         static_cast<float *>(dl)[at] = v;
 }
 
-// One warp per token.  With q_j = s_j / sum of the chosen s (normalised) the
+// One warp per token; bound by the writing of dlogits: 16384 x 256 BF16 in 7.7 us.
+// With q_j = s_j / sum of the chosen s (normalised) the
 // gradient of a chosen score is ds_j = scale (dw_j - sum_i dw_i q_i) / sum;
 // through the softmax that is dl_j = scale q_j (dw_j - sum_i dw_i q_i) and 0
 // elsewhere, which needs the chosen logits only.  Not normalised, softmax:
@@ -377,7 +381,10 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_count_kernel(
 // pairs per expert in its own counters, the counters become start rows (over the
 // experts, then the CTAs, then the warps), and the warp goes over its run again in
 // order, a pair's row being its expert's counter plus its rank among the lanes
-// with the same expert.  counts: of every CTA (nullptr with one CTA).
+// with the same expert.  counts: of every CTA (nullptr with one CTA).  Deterministic
+// (the only atomics are counts).  Bound by latency: 524288 pairs, 256 experts in
+// about 4 + 10 us (128 CTAs; the first kernel counts), 512 pairs in 7 us.  One
+// cluster of 16 CTAs took 37 us: too few SMs for the instructions.
 __global__ void __launch_bounds__(kSortThreads) moe_sort_rows_kernel(
     const int32_t *__restrict__ ids, int64_t n, int32_t E, const uint32_t *__restrict__ counts,
     int64_t *__restrict__ offs, int32_t *__restrict__ pair_of_row, int32_t *__restrict__ row_of_pair)
