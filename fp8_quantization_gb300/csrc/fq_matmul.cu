@@ -20,8 +20,11 @@ constexpr int kRowsM = 128;       // rows of c of a CTA (its TMEM lanes)
 constexpr int kBlockK = 128;      // one scale block, one pipeline stage
 constexpr int kPromoteWarps = 8;  // two warpgroups
 constexpr int kMmThreads = (kPromoteWarps + 4) * 32;
-// 384 threads x 168 registers at launch = 64512; 256 x 200 + 128 x 104 as well
-constexpr int kPromoteRegs = 200, kOtherRegs = 104;
+// Registers of a promoting and of another thread: 384 threads x 168 at launch =
+// 64512 = 256 x 200 + 128 x 104 = 256 x 208 + 128 x 88.  The other roles' spills
+// cost 10 to 20 % (at 56); with a scale per column the promoting warps need more.
+constexpr int promote_regs(bool col_scale) { return col_scale ? 208 : 200; }
+constexpr int other_regs(bool col_scale) { return col_scale ? 88 : 104; }
 constexpr int kRaster = 8;        // row tiles walked together over the columns
 constexpr int kScaleBlocks = 4;   // blocks whose scales are fetched together
 constexpr int kBoxCols = 32;      // columns of c that a warp writes at once
@@ -280,7 +283,7 @@ __device__ __forceinline__ float4 load_scales(const float *s, int64_t step, int3
 // Why so: pairs of CTAs halve the traffic of b (one CTA a tile: 415 us before the
 // rest); 256 accumulator columns need 128 registers a thread, so the other roles
 // give theirs up, down to 104 (at 56 they spill, and the kernel takes 10 to 20 %
-// longer); 16 columns less pressure but more waits a column (192-column tiles: 410
+// longer); 192-column tiles wait more often per column (410
 // us); half-tile MMAs read a twice (500 us); 16 adding warps have too few registers
 // (414 us and more).
 template <int kCtas, Mode kMode, bool kF32>
@@ -344,7 +347,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     TileWalk<kMode, kCtas> walk(blockIdx.x / kCtas, gridDim.x / kCtas, mt, nt, ntiles);
 
     if (wid >= kPromoteWarps) {
-        regs_down<kOtherRegs>();
+        regs_down<other_regs(kColScale)>();
         if (wid == kCopyWarp) {
             const uint32_t full0 = smem_u32(t.full), empty0 = smem_u32(t.empty);
             const uint32_t fill0 = kCtas == 1 ? full0 : cluster_addr(t.full, 0);
@@ -464,7 +467,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         }
         __syncwarp();
     } else {
-        regs_up<kPromoteRegs>();
+        regs_up<promote_regs(kColScale)>();
         const int half = wid >> 2;
         const uint32_t lane_base =
             tmem + (static_cast<uint32_t>(32 * (wid & 3)) << 16) + half * kCols;
@@ -475,8 +478,42 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         const uint32_t read0 = kCtas == 1 ? smem_u32(t.acc_empty) : cluster_addr(t.acc_empty, 0);
         const uint32_t scale_full0 = smem_u32(t.scale_full), scale_empty0 = smem_u32(t.scale_empty);
         uint32_t it = 0, gq = 0, nbox = 0;
-        while (!*abort && walk.more()) {
-            const Tile tl = walk.next(p, off, first);
+        // The scales of the row and (kTileScale) of the weight tile that the columns
+        // lie in, fetched two blocks ahead: those of a tile's first blocks before the
+        // output of the tile before.
+        const int64_t step = kMode == kWgrad ? p.R : 1;
+        const float *sa = nullptr, *sb = nullptr;
+        float a0 = 0.0f, a1 = 0.0f, b0 = 1.0f, b1 = 1.0f;
+        auto open_tile = [&](const Tile &t) {
+            const int32_t row = t.row + rank * kRowsM + 32 * (wid & 3) + lane;
+            if (kMode == kWgrad)
+                sa = p.sa + static_cast<int64_t>(t.xblk) * p.R + min(row, p.R - 1);
+            else
+                sa = p.sa + static_cast<int64_t>(min(row, p.M - 1)) * p.KB;
+            if (!kColScale)
+                sb = p.sb + (static_cast<int64_t>(t.g) * p.sb_rows +
+                             min((t.n0 + half * kCols) / 128, p.sb_rows - 1)) * p.KB;
+            if (t.blocks > 0) {
+                a0 = __ldg(sa);
+                if (!kColScale)
+                    b0 = __ldg(sb);
+            }
+            if (t.blocks > 1) {
+                a1 = __ldg(sa + step);
+                if (!kColScale)
+                    b1 = __ldg(sb + 1);
+            }
+            sa += 2 * step;
+            sb += 2;
+        };
+        bool more = walk.more();
+        Tile next = {};
+        if (more) {
+            next = walk.next(p, off, first);
+            open_tile(next);
+        }
+        while (more && !*abort) {
+            const Tile tl = next;
             const int32_t blocks = tl.blocks;
             const int32_t col0 = tl.n0 + half * kCols;
             const int32_t row0 = tl.row + rank * kRowsM + 32 * (wid & 3);
@@ -484,27 +521,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 #pragma unroll
             for (int e = 0; e < kCols / 2; e++)
                 acc[e] = 0;
-            // the scales of the row and (kTileScale) of the weight tile that the
-            // columns lie in, fetched two blocks ahead
-            const int64_t step = kMode == kWgrad ? p.R : 1;
-            const float *sa = kMode == kWgrad
-                                  ? p.sa + static_cast<int64_t>(tl.xblk) * p.R + min(row0 + lane, p.R - 1)
-                                  : p.sa + static_cast<int64_t>(min(row0 + lane, p.M - 1)) * p.KB;
-            const float *sb = p.sb + (static_cast<int64_t>(tl.g) * p.sb_rows +
-                                      min(col0 / 128, p.sb_rows - 1)) * p.KB;
-            float a0 = 0.0f, a1 = 0.0f, b0 = 1.0f, b1 = 1.0f;
-            if (blocks > 0) {
-                a0 = __ldg(sa);
-                if (!kColScale)
-                    b0 = __ldg(sb);
-            }
-            if (blocks > 1) {
-                a1 = __ldg(sa + step);
-                if (!kColScale)
-                    b1 = __ldg(sb + 1);
-            }
-            sa += 2 * step;
-            sb += 2;
             // A wait that gives up does not leave the loop (the other warps' waits
             // end soon as well); the flag is looked at behind it.
 #pragma unroll 1
@@ -565,6 +581,11 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     mbar_arrive_cluster(scale_empty0 + 8 * slot, leader);
                     gq++;
                 }
+            }
+            more = walk.more();
+            if (more) {
+                next = walk.next(p, off, first);
+                open_tile(next);
             }
             const bool ok = __all_sync(0xffffffffu, *abort == 0);
             const int32_t rows = min(32, tl.end - row0);
