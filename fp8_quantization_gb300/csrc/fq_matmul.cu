@@ -1005,6 +1005,21 @@ fq_status launch_few(const uint8_t *a, const uint8_t *b, int64_t K, const MmArgs
     return launch_status();
 }
 
+// Whether tiles of one CTA (128 x 128) finish before tiles of a pair (256 x 256):
+// rounds over the SMs, a round of pairs counting for two, times `percent` of a
+// pair's time for the same work.  Measured both ways: forward 125 (N x K 4096 x
+// 7168, 512 rows: 128 tiles, one round 21.4 us, pairs 27.0; 1024 rows: 256 tiles, two
+// rounds 37.6, pairs 28.2), weight gradient 104 (1003 tokens, 8 x 1408 x 2048: 10
+// rounds 28.1 us, 6 of pairs 30.9; 16384 tokens, 16 x 2048 x 2048: 27 rounds 150, 14 of
+// pairs 144).
+inline bool one_cta_tiles(int64_t rows, int64_t cols, int64_t groups, int percent)
+{
+    const int64_t sms = sm_count(), pairs = sms > 1 ? sms / 2 : 1;
+    const int64_t one = (rows + 127) / 128 * ((cols + 127) / 128) * groups;
+    const int64_t two = (rows + 255) / 256 * ((cols + 255) / 256) * groups;
+    return (one + sms - 1) / sms * percent < (two + pairs - 1) / pairs * 200;
+}
+
 template <Mode kMode, bool kF32>
 fq_status launch_forward(const uint8_t *a, const uint8_t *b, int64_t K, const MmArgs &p,
                          cudaStream_t st)
@@ -1014,8 +1029,7 @@ fq_status launch_forward(const uint8_t *a, const uint8_t *b, int64_t K, const Mm
     //   rows 32: few rows 9.9, one CTA a tile 19.9, pairs 26.4
     //   rows 64: 12.3 (K split eight ways), 19.9, 26.5; but 14336 x 4096, where it
     //            is not split: 24.0, 14.4, 18.8; 32 groups of 64: 176, 167, 197
-    //   rows 512: one CTA 21.4, pairs 27.0 (128 and 32 tiles); rows 1024: 37.6, 28.2
-    //   32 groups of 128 rows: 175, 201; of 256: 288, 227
+    //   32 groups of 128 rows: one CTA a tile 175, pairs 201; of 256: 288, 227
     const int64_t mean = (static_cast<int64_t>(p.M) + p.G - 1) / p.G;
     const int64_t sms = sm_count(), nt = (p.N + 127) / 128;
     const int64_t b_rows = static_cast<int64_t>(p.G) * p.N;
@@ -1025,7 +1039,7 @@ fq_status launch_forward(const uint8_t *a, const uint8_t *b, int64_t K, const Mm
         return launch_few<32, kMode, kF32>(a, b, K, p, st);
     if (mean <= 64 && 2 * nt * p.G <= sms)
         return launch_few<64, kMode, kF32>(a, b, K, p, st);
-    if (p.G > 1 ? mean <= 128 : (mean + 127) / 128 * nt <= sms)
+    if (p.G > 1 ? mean <= 128 : one_cta_tiles(p.M, p.N, 1, 125))
         return launch_matmul<1, kMode, kF32>(a, p.M, b, b_rows, K, p.M, p, st);
     return launch_matmul<2, kMode, kF32>(a, p.M, b, b_rows, K, p.M, p, st);
 }
@@ -1233,7 +1247,7 @@ extern "C" fq_status fp8_matmul_wgrad(const uint8_t *aT, const float *aT_scale, 
     p.R = static_cast<int32_t>(N);
     p.N = static_cast<int32_t>(K);
     p.add = accumulate;
-    if (mt * nt * G <= sm_count())  // the smaller tiles fill more SMs
+    if (one_cta_tiles(N, K, G, 104))
         return c_f32 ? launch_matmul<1, kWgrad, true>(wa, N, wb, K, pitch, G * N, p, st)
                      : launch_matmul<1, kWgrad, false>(wa, N, wb, K, pitch, G * N, p, st);
     return c_f32 ? launch_matmul<2, kWgrad, true>(wa, N, wb, K, pitch, G * N, p, st)
