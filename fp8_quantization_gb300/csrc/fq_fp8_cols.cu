@@ -10,9 +10,10 @@
 //   a block holding NaN or Inf gets s = NaN and codes 0x7F.
 //
 // 2 bytes read and 1 written per element, 4 bytes written per block and feature:
-// 65536 x 2048 in 85 us, 4.8 TB/s.  HBM and the instructions share the bound (issue
-// slots 60 % busy, 4 CTAs per SM).  Written as 4-byte words, a warp a row, it took
-// 172 us; with the divisions in every thread 94 us.
+// 65536 x 2048 in 83 us, 4.9 TB/s.  HBM and the instructions share the bound (issue
+// slots 60 % busy).  5 CTAs per SM (48 registers; 4 CTAs: 85 us, 6 with spills: 95).
+// Written as 4-byte words, a warp a row, it took 172 us; with the divisions in every
+// thread 94 us.
 #include <cfloat>
 
 #include "fq_tc.cuh"
@@ -44,7 +45,7 @@ __device__ __forceinline__ uint32_t cvt_e4m3_pair(float lo, float hi)
 // conversion takes two tokens of a feature at a time, so nothing is
 // transposed in registers).  Rows of the transposed tile start at any byte of
 // yT: they are written as aligned 16-byte pieces, the bytes at both ends alone.
-__global__ void __launch_bounds__(kThreads) fp8_quantize_cols_kernel(
+__global__ void __launch_bounds__(kThreads, 5) fp8_quantize_cols_kernel(
     const uint16_t *__restrict__ x, int32_t M, int32_t K, const int64_t *__restrict__ offs,
     int32_t G, uint8_t *__restrict__ yT, float *__restrict__ scale, int64_t cap, int32_t *dev_status)
 {
