@@ -65,94 +65,133 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// Largest key of the warp and the lowest index that has it; 0 if none.
-__device__ __forceinline__ uint32_t warp_best(uint32_t key, int idx, int &best)
+// Largest key of the warp and the lowest lane that has it; 0 if none.
+__device__ __forceinline__ uint32_t warp_best(uint32_t key, int &lane)
 {
     const uint32_t m = __reduce_max_sync(kFull, key);
-    best = static_cast<int>(__reduce_min_sync(kFull, key == m ? static_cast<unsigned>(idx) : 0x7fffffffu));
+    lane = __ffs(__ballot_sync(kFull, key == m)) - 1;
     return m;
 }
 
-// One warp per token; lane l holds the experts l + 32 i.  kVals >= E / 32.  A choice
-// is two warp reductions (the largest key, the lowest index that has it), so ties
-// need no sort.  Bound by those k rounds of dependent instructions, not by memory:
-// 16384 x 256 BF16 logits, k = 8, in 20 us (8.4 MB); 8 tokens with groups in 8 us.
-template <int kVals, bool kBf16, bool kSigmoid, bool kNorm>
-__global__ void __launch_bounds__(kThreads) moe_route_kernel(const RouteArgs p)
+// Lane l's logits kVals l .. of a row, -inf past its E.  Rows of whole chunks of 16
+// bytes (of a lane's share where that is less) start at a multiple of them.
+template <bool kBf16, int kVals>
+__device__ __forceinline__ void load_logits(const void *logits, int64_t row, int32_t E, float (&l)[kVals])
 {
+    constexpr int size = kBf16 ? 2 : 4, chunk = kVals * size < 16 ? kVals : 16 / size;
+    const int e0 = (threadIdx.x & 31) * kVals;
+    if constexpr (chunk * size >= 4) {
+        if (E % chunk == 0) {
+            const char *at = static_cast<const char *>(logits) + (row + e0) * size;
+#pragma unroll
+            for (int i0 = 0; i0 < kVals; i0 += chunk) {
+                const bool in = e0 + i0 < E;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (in) {
+                    if constexpr (chunk * size == 16)
+                        v = __ldg(reinterpret_cast<const uint4 *>(at + i0 * size));
+                    else if constexpr (chunk * size == 8) {
+                        const uint2 h = __ldg(reinterpret_cast<const uint2 *>(at));
+                        v.x = h.x, v.y = h.y;
+                    } else
+                        v.x = __ldg(reinterpret_cast<const uint32_t *>(at));
+                }
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < chunk; i++) {
+                    const uint32_t word = w[kBf16 ? i / 2 : i];
+                    const float x = !kBf16 ? __uint_as_float(word) : i & 1 ? bf16_hi(word) : bf16_lo(word);
+                    l[i0 + i] = in ? x : -INFINITY;
+                }
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kVals; i++)
+        l[i] = e0 + i < E ? load_logit<kBf16>(logits, row + e0 + i) : -INFINITY;
+}
+
+// One warp per token; lane l holds the kVals experts from kVals l on, so that ties
+// of the warp's largest key go to the lowest lane: one maximum and one ballot a
+// choice.  A lane's keys are sorted once in runs of four (stable), and the choices
+// look at the runs' heads only.  Bound by the integer pipe (80 % busy; about 700
+// instructions a token), not by memory: 16384 x 256 BF16 logits (8.4 MB), k = 8, in
+// 14.0 us; FP32, sigmoid, bias, the best 4 of 8 groups 26 us, 8 tokens of it 4.8.
+// With every lane's keys looked through in each round, and the experts strided over
+// the lanes (a second reduction for ties): 18.1, 46 and 6.5 us.  Left to itself the
+// compiler keeps the registers at 48 to 128 and spills: 1000 experts 53 us for 43.
+template <int kVals, bool kBf16, bool kSigmoid, bool kNorm>
+__global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 2) moe_route_kernel(const RouteArgs p)
+{
+    constexpr int kRun = kVals < 4 ? kVals : 4, kRuns = kVals / kRun;
     griddep_wait();  // the previous kernel's outputs (PDL launch)
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, e0 = lane * kVals;
     const int per_group = p.E / p.n_groups;
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < p.T;
          t += static_cast<int64_t>(gridDim.x) * kWarps) {
         const int64_t row = t * p.E;
         float l[kVals];
+        load_logits<kBf16, kVals>(p.logits, row, p.E, l);
         float mx = -FLT_MAX;
 #pragma unroll
         for (int i = 0; i < kVals; i++) {
-            const int e = lane + 32 * i;
-            l[i] = e < p.E ? load_logit<kBf16>(p.logits, row + e) : -INFINITY;
-            if (l[i] > kMasked)
-                mx = fmaxf(mx, fminf(l[i], FLT_MAX));
+            l[i] = l[i] > kMasked ? fminf(l[i], FLT_MAX) : -INFINITY;
+            mx = fmaxf(mx, l[i]);
         }
-        float sum = 1.0f;
         if (!kSigmoid) {
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1)
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
-            sum = 0.0f;
         }
-        uint32_t key[kVals];
+        float sum = 0.0f;
+        uint32_t key[kVals];  // of the scores, which are 0 or above: 0 where masked
 #pragma unroll
         for (int i = 0; i < kVals; i++) {
-            const bool ok = l[i] > kMasked;
-            float s = 0.0f;
-            if (ok)
-                s = kSigmoid ? sigmoid_score(fminf(l[i], FLT_MAX)) : expf(fminf(l[i], FLT_MAX) - mx);
+            const float s = kSigmoid ? sigmoid_score(l[i]) : expf(l[i] - mx);
             if (!kSigmoid)
                 sum += s;
-            l[i] = s;
-            key[i] = ok;
+            key[i] = l[i] > -INFINITY ? __float_as_uint(s) | 0x80000000u : 0u;
         }
-        if (!kSigmoid)
+        if (!kSigmoid && (!kNorm || p.bias))
             sum = warp_sum(sum);
+        if (p.bias) {
 #pragma unroll
-        for (int i = 0; i < kVals; i++) {
-            float c = l[i];
-            const int e = lane + 32 * i;
-            if (p.bias && e < p.E)
-                c = (kSigmoid ? c : __fdiv_rn(c, sum)) + __ldg(p.bias + e);
-            key[i] = key[i] && c > -INFINITY ? order_key(c) : 0u;
+            for (int i = 0; i < kVals; i++)
+                if (key[i]) {
+                    const float s = key_value(key[i]);
+                    const float c = (kSigmoid ? s : __fdiv_rn(s, sum)) + __ldg(p.bias + e0 + i);
+                    key[i] = c > -INFINITY ? order_key(c) : 0u;
+                }
         }
 
         if (p.n_groups > 1) {
-            // score of group g in lane g
-            uint32_t score = 0;
-            for (int g = 0; g < p.n_groups; g++) {
-                const int lo = g * per_group, hi = lo + per_group;
-                uint32_t m = 0;
-                int at = 0;
+            // the lane's two best keys among its experts from `lo` to `hi`
+            uint32_t m1 = 0, m2 = 0;
+            const auto best_two = [&](int lo, int hi) {
+                m1 = m2 = 0;
 #pragma unroll
                 for (int i = 0; i < kVals; i++) {
-                    const int e = lane + 32 * i;
-                    if (e >= lo && e < hi && key[i] > m) {
-                        m = key[i];
-                        at = e;
-                    }
+                    const uint32_t v = e0 + i >= lo && e0 + i < hi ? key[i] : 0u;
+                    m2 = max(m2, min(m1, v));
+                    m1 = max(m1, v);
                 }
-                int b1;
-                const uint32_t k1 = warp_best(m, at, b1);
+            };
+            const bool whole = per_group % kVals == 0;  // a lane's experts are of one group
+            if (whole)
+                best_two(0, p.E);
+            uint32_t score = 0;  // of group g in lane g
+            for (int g = 0; g < p.n_groups; g++) {
+                const int lo = g * per_group, hi = lo + per_group;
+                if (!whole)
+                    best_two(lo, hi);
+                const bool in = !whole || (e0 >= lo && e0 < hi);
+                int l1;
+                const uint32_t k1 = warp_best(in ? m1 : 0u, l1);
                 uint32_t sk = k1;
                 if (p.top == 2) {
-                    m = 0;
-#pragma unroll
-                    for (int i = 0; i < kVals; i++) {
-                        const int e = lane + 32 * i;
-                        if (e >= lo && e < hi && e != b1 && key[i] > m)
-                            m = key[i];
-                    }
-                    const uint32_t k2 = __reduce_max_sync(kFull, m);
+                    const uint32_t k2 = __reduce_max_sync(kFull, !in ? 0u : lane == l1 ? m2 : m1);
                     if (k2) {
                         const float v = key_value(k1) + key_value(k2);
                         sk = order_key(v == 0.0f ? 0.0f : v);
@@ -164,39 +203,79 @@ __global__ void __launch_bounds__(kThreads) moe_route_kernel(const RouteArgs p)
             uint32_t kept = 0;
             for (int j = 0; j < p.keep; j++) {
                 int g;
-                if (!warp_best(score, lane, g))
+                if (!warp_best(score, g))
                     break;
                 kept |= 1u << g;
                 if (lane == g)
                     score = 0;
             }
+            int g = e0 / per_group, end = (g + 1) * per_group;
 #pragma unroll
             for (int i = 0; i < kVals; i++) {
-                const int e = lane + 32 * i;
-                if (e < p.E && !((kept >> (e / per_group)) & 1u))
+                if (e0 + i == end) {
+                    g++;
+                    end += per_group;
+                }
+                if (e0 + i < p.E && !((kept >> g) & 1u))
                     key[i] = 0;
             }
         }
 
+        // runs of four keys in descending order, equal ones as they stand, with the
+        // places they had, a byte each
+        uint32_t place[kRuns];
+#pragma unroll
+        for (int q = 0; q < kRuns; q++) {
+            uint32_t at[kRun];
+#pragma unroll
+            for (int i = 0; i < kRun; i++)
+                at[i] = q * kRun + i;
+#pragma unroll
+            for (int n = kRun - 1; n > 0; n--)
+#pragma unroll
+                for (int i = 0; i < n; i++) {
+                    uint32_t &a = key[q * kRun + i], &b = key[q * kRun + i + 1];
+                    const bool swap = b > a;
+                    const uint32_t hi = max(a, b), lo = min(a, b), x = at[i];
+                    a = hi;
+                    b = lo;
+                    at[i] = swap ? at[i + 1] : x;
+                    at[i + 1] = swap ? x : at[i + 1];
+                }
+            place[q] = 0;
+#pragma unroll
+            for (int i = 0; i < kRun; i++)
+                place[q] |= at[i] << (8 * i);
+        }
+
         int id = -1;  // of slot `lane`
         for (int j = 0; j < p.k; j++) {
-            uint32_t m = 0;
-            int at = 0;
+            uint32_t m = key[0], at = place[0];
+            int run = 0;
 #pragma unroll
-            for (int i = 0; i < kVals; i++)
-                if (key[i] > m) {
-                    m = key[i];
-                    at = lane + 32 * i;
-                }
-            int e;
-            if (!warp_best(m, at, e))
+            for (int q = 1; q < kRuns; q++) {
+                const bool more = key[q * kRun] > m;
+                m = more ? key[q * kRun] : m;
+                at = more ? place[q] : at;
+                run = more ? q : run;
+            }
+            int src;
+            if (!warp_best(m, src))
                 break;
+            const int e = __shfl_sync(kFull, e0 + static_cast<int>(at & 255u), src);
             if (lane == j)
                 id = e;
+            if (lane != src)
+                run = -1;
 #pragma unroll
-            for (int i = 0; i < kVals; i++)
-                if (lane + 32 * i == e)
-                    key[i] = 0;
+            for (int q = 0; q < kRuns; q++)
+                if (run == q) {
+#pragma unroll
+                    for (int i = 0; i < kRun - 1; i++)
+                        key[q * kRun + i] = key[q * kRun + i + 1];
+                    key[q * kRun + kRun - 1] = 0;
+                    place[q] >>= 8;
+                }
         }
         float w = 0.0f;
         if (id >= 0) {
@@ -383,8 +462,8 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_count_kernel(
 // order, a pair's row being its expert's counter plus its rank among the lanes
 // with the same expert.  counts: of every CTA (nullptr with one CTA).  Deterministic
 // (the only atomics are counts).  Bound by latency: 524288 pairs, 256 experts in
-// about 4 + 10 us (128 CTAs; the first kernel counts), 512 pairs in 7 us.  One
-// cluster of 16 CTAs took 37 us: too few SMs for the instructions.
+// 13.6 us with the counting kernel (128 CTAs), 512 pairs in 4.4 us.  One cluster of
+// 16 CTAs took 37 us: too few SMs for the instructions.
 __global__ void __launch_bounds__(kSortThreads) moe_sort_rows_kernel(
     const int32_t *__restrict__ ids, int64_t n, int32_t E, const uint32_t *__restrict__ counts,
     int64_t *__restrict__ offs, int32_t *__restrict__ pair_of_row, int32_t *__restrict__ row_of_pair)
@@ -409,6 +488,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_rows_kernel(
     for (int e0 = 0; e0 < E; e0 += kSortThreads) {
         const int e = e0 + tid;
         uint32_t before = 0, all = 0;  // the expert's pairs: of the CTAs before, of all
+        uint32_t from[kSortWarps];     // of this CTA's warps before
         if (e < E) {
             if (counts) {
                 const int ctas = gridDim.x, self = blockIdx.x;
@@ -419,12 +499,14 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_rows_kernel(
                     all += v;
                 }
             }
-            uint32_t run = 0;
+            uint32_t c[kSortWarps], run = 0;
+#pragma unroll
+            for (int w = 0; w < kSortWarps; w++)
+                c[w] = count[w * E + e];
 #pragma unroll
             for (int w = 0; w < kSortWarps; w++) {
-                const uint32_t c = count[w * E + e];
-                count[w * E + e] = run;
-                run += c;
+                from[w] = run;
+                run += c[w];
             }
             if (!counts)
                 all = run;
@@ -451,7 +533,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_rows_kernel(
                 offs[e] = start;
 #pragma unroll
             for (int w = 0; w < kSortWarps; w++)
-                count[w * E + e] += start + before;
+                count[w * E + e] = start + before + from[w];
         }
         __syncthreads();
     }
