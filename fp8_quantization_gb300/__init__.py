@@ -171,6 +171,17 @@ def _empty(shape, dtype, like: torch.Tensor):
     return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _out(t: torch.Tensor | None, shape: tuple, dtype, like: torch.Tensor, name: str):
+    """The output `t` checked, or a new one (which needs no check)."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    numel = 1
+    for n in shape:
+        numel *= n
+    _need(t, dtype, name, numel=numel)
+    return t
+
+
 # ---------------------------------------------------------------- MXFP4
 # Sizes are checked wherever the block size divides the tensor; a size the
 # block does not divide is passed on, and the library rejects it with
@@ -208,7 +219,7 @@ def fp4_to_fp8_rows(q: torch.Tensor, s: torch.Tensor, exp_offset_k: int = 0,
 
 
 def fp4_to_fp8_cols_scale_capacity(M: int, G: int) -> int:
-    return int(abi().fp4_to_fp8_cols_scale_capacity(int(M), int(G)))
+    return int((_lib or abi()).fp4_to_fp8_cols_scale_capacity(int(M), int(G)))
 
 
 def fp4_to_fp8_cols_launch_count(K: int) -> int:
@@ -472,8 +483,7 @@ def fp8_matmul(y: torch.Tensor, ys: torch.Tensor, w: torch.Tensor, ws: torch.Ten
     if tuple(ws.shape) not in (tiles, rows):
         raise ValueError(f"ws must have shape {tiles} or {rows}, got {tuple(ws.shape)}")
     dt = _out_dtype(out, out_dtype)
-    out = _empty((M, N), dt, y) if out is None else out
-    _need(out, dt, "out", numel=M * N)
+    out = _out(out, (M, N), dt, y, "out")
     _dev_status(dev_status)
     _on_device(y=y, ys=ys, w=w, ws=ws, group_offsets=group_offsets, out=out,
                dev_status=dev_status)
@@ -493,22 +503,24 @@ def fp8_quantize_cols(x: torch.Tensor, group_offsets: torch.Tensor | None = None
     M, K = x.shape
     G = 1 if group_offsets is None else _groups(group_offsets)
     cap = fp4_to_fp8_cols_scale_capacity(M, G)
-    yT = _empty((K, M), torch.uint8, x) if yT is None else yT
-    yT_scale = _empty((cap, K), torch.float32, x) if yT_scale is None else yT_scale
-    _need(yT, torch.uint8, "yT", numel=K * M)
-    _need(yT_scale, torch.float32, "yT_scale", 2)
-    if yT_scale.shape[1] != K or yT_scale.shape[0] < cap:
-        raise ValueError(f"yT_scale must be [>= {cap}, {K}], got {tuple(yT_scale.shape)}")
+    yT = _out(yT, (K, M), torch.uint8, x, "yT")
+    if yT_scale is None:
+        yT_scale = _empty((cap, K), torch.float32, x)
+    else:
+        _need(yT_scale, torch.float32, "yT_scale", 2)
+        if yT_scale.shape[1] != K or yT_scale.shape[0] < cap:
+            raise ValueError(f"yT_scale must be [>= {cap}, {K}], got {tuple(yT_scale.shape)}")
+        cap = yT_scale.shape[0]
     _dev_status(dev_status)
     _on_device(x=x, group_offsets=group_offsets, yT=yT, yT_scale=yT_scale, dev_status=dev_status)
-    _call("fp8_quantize_cols", _p(x), M, K, _p(group_offsets), G, _p(yT), _p(yT_scale),
-          int(yT_scale.shape[0]), _p(dev_status), _stream())
+    _call("fp8_quantize_cols", _p(x), M, K, _p(group_offsets), G, _p(yT), _p(yT_scale), cap,
+          _p(dev_status), _stream())
     return yT, yT_scale
 
 
 def fp8_matmul_wgrad_workspace(M: int, N: int, K: int, G: int) -> int:
     """Bytes of workspace fp8_matmul_wgrad needs (-1 for a rejected shape)."""
-    return int(abi().fp8_matmul_wgrad_workspace(int(M), int(N), int(K), int(G)))
+    return int((_lib or abi()).fp8_matmul_wgrad_workspace(int(M), int(N), int(K), int(G)))
 
 
 def fp8_matmul_wgrad(aT: torch.Tensor, aT_scale: torch.Tensor, bT: torch.Tensor,
@@ -535,8 +547,7 @@ def fp8_matmul_wgrad(aT: torch.Tensor, aT_scale: torch.Tensor, bT: torch.Tensor,
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     dt = _out_dtype(out, out_dtype)
-    out = _empty((G, N, K), dt, aT) if out is None else out
-    _need(out, dt, "out", numel=G * N * K)
+    out = _out(out, (G, N, K), dt, aT, "out")
     need = fp8_matmul_wgrad_workspace(M, N, K, G)
     if group_offsets is None and M % 16 == 0 and M > 0:
         need = 0  # read in place
@@ -577,10 +588,8 @@ def moe_route(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None,
     runs of experts, weights divided by their sum if `renormalize`, times
     `scale`.  A slot without an available expert has id -1 and weight 0."""
     T, E = _logits(logits, score)
-    weights = _empty((T, k), torch.float32, logits) if weights is None else weights
-    ids = _empty((T, k), torch.int32, logits) if ids is None else ids
-    _need(weights, torch.float32, "weights", numel=T * k)
-    _need(ids, torch.int32, "ids", numel=T * k)
+    weights = _out(weights, (T, k), torch.float32, logits, "weights")
+    ids = _out(ids, (T, k), torch.int32, logits, "ids")
     if bias is not None:
         _need(bias, torch.float32, "bias", numel=E)
     _on_device(logits=logits, bias=bias, weights=weights, ids=ids)
@@ -600,8 +609,7 @@ def moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.
     k = ids.shape[1]
     _need(ids, torch.int32, "ids", shape=(T, k))
     _need(dweights, torch.float32, "dweights", shape=(T, k))
-    dlogits = _empty((T, E), logits.dtype, logits) if dlogits is None else dlogits
-    _need(dlogits, logits.dtype, "dlogits", numel=T * E)
+    dlogits = _out(dlogits, (T, E), logits.dtype, logits, "dlogits")
     _on_device(logits=logits, ids=ids, dweights=dweights, dlogits=dlogits)
     _call("moe_route_backward", _p(logits), int(logits.dtype == torch.float32), T, E, _p(ids),
           _p(dweights), k, int(score == "sigmoid"), int(bool(renormalize)), float(scale),
@@ -611,7 +619,7 @@ def moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.
 
 def moe_sort_rows_workspace(n: int, n_experts: int) -> int:
     """Bytes of workspace moe_sort_rows needs for n pairs (-1: rejected)."""
-    return int(abi().moe_sort_rows_workspace(int(n), int(n_experts)))
+    return int((_lib or abi()).moe_sort_rows_workspace(int(n), int(n_experts)))
 
 
 def moe_sort_rows(ids: torch.Tensor, n_experts: int, group_offsets: torch.Tensor | None = None,
@@ -624,16 +632,14 @@ def moe_sort_rows(ids: torch.Tensor, n_experts: int, group_offsets: torch.Tensor
     holds token pair_of_row[r] // k; ids outside [0, E) get no row (-1)."""
     _need(ids, torch.int32, "ids")
     n, E = ids.numel(), int(n_experts)
-    group_offsets = _empty((max(E, 0) + 1,), torch.int64, ids) if group_offsets is None else group_offsets
-    pair_of_row = _empty((n,), torch.int32, ids) if pair_of_row is None else pair_of_row
-    row_of_pair = torch.empty_like(ids) if row_of_pair is None else row_of_pair
-    _need(group_offsets, torch.int64, "group_offsets", numel=E + 1 if E > 0 else None)
-    _need(pair_of_row, torch.int32, "pair_of_row", numel=n)
-    _need(row_of_pair, torch.int32, "row_of_pair", numel=n)
+    group_offsets = _out(group_offsets, (max(E, 0) + 1,), torch.int64, ids, "group_offsets")
+    pair_of_row = _out(pair_of_row, (n,), torch.int32, ids, "pair_of_row")
+    row_of_pair = _out(row_of_pair, tuple(ids.shape), torch.int32, ids, "row_of_pair")
     need = moe_sort_rows_workspace(n, E)
-    if workspace is None and need > 0:
-        workspace = _empty((need,), torch.uint8, ids)
-    if workspace is not None:
+    if workspace is None:
+        if need > 0:
+            workspace = _empty((need,), torch.uint8, ids)
+    else:
         _need(workspace, torch.uint8, "workspace")
         if workspace.numel() < need:
             raise ValueError(f"workspace must hold {need} bytes, got {workspace.numel()}")
