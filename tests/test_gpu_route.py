@@ -167,6 +167,42 @@ def grad64(logits, ids, dw, score, renorm, scale):
     return s * (full - (full * s).sum(1, keepdim=True)), s * (fmag + (fmag * s).sum(1, keepdim=True))
 
 
+@pytest.mark.parametrize("E,k,groups,keep,gtop", [
+    (33, 4, 1, 1, 1), (64, 8, 4, 2, 2), (96, 6, 1, 1, 1), (130, 8, 5, 2, 2), (200, 8, 8, 3, 1),
+    (256, 32, 8, 4, 2), (250, 8, 25, 20, 2), (500, 9, 1, 1, 1), (512, 8, 32, 5, 2), (1000, 32, 1, 1, 1),
+    (1024, 8, 4, 1, 2)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_ties_go_to_the_lowest_index(fq, E, k, groups, keep, gtop, score, dtype):
+    """Rows of four values (so that every choice ties with others, in its lane's
+    run and across lanes) with every fifth logit masked; rows with fewer experts
+    than slots.  The sums of two of the four scores lie further apart than their
+    rounding, so the groups' order is known too."""
+    T = 40
+    rng = np.random.default_rng(E)
+    l = rng.integers(0, 4, (T, E)).astype(np.float64)
+    l[rng.random((T, E)) < 0.2] = -np.inf
+    l[1] = 2.0
+    l[2, 5:] = -np.inf
+    l[3, : E - 3] = -np.inf
+    l[4] = -np.inf
+    _, ids = fq.moe_route(torch.tensor(l, device="cuda").to(dtype), k, score=score, n_groups=groups,
+                          keep_groups=keep, group_top=gtop)
+    with np.errstate(invalid="ignore"):
+        s = 1 / (1 + np.exp(-l)) if score == "sigmoid" else np.exp(l - 3)
+    want = np.full((T, k), -1)
+    for t in range(T):
+        c = np.where(l[t] > -np.inf, s[t], -1.0)
+        if groups > 1:
+            best = -np.sort(-c.reshape(groups, -1), axis=1)[:, :gtop]
+            total = np.where(best[:, 0] < 0, -1.0, np.maximum(best, 0).sum(1))
+            kept = [g for g in np.argsort(-total, kind="stable")[:keep] if total[g] >= 0]
+            c = np.where(np.isin(np.arange(E) // (E // groups), kept), c, -1.0)
+        order = [e for e in np.argsort(-c, kind="stable")[:k] if c[e] >= 0]
+        want[t, : len(order)] = order
+    assert np.array_equal(ids.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("case", CASES)
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
