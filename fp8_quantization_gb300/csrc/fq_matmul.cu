@@ -279,7 +279,7 @@ __device__ __forceinline__ float4 load_scales(const float *s, int64_t step, int3
 // latency, which two warps a scheduler do not hide.  16384 x 4096 x 7168: 337 us
 // (2.86 PFLOP/s) with the L2 flushed, 375 us back to back at the lower clocks that
 // this draws; without scaling and adding the same loop takes 285 us.  With a scale
-// per column it is twice the FMAs and a shared load per four columns: 566 us.
+// per column it is twice the FMAs and a shared load per four columns: 540 us.
 // Why so: pairs of CTAs halve the traffic of b (one CTA a tile: 415 us before the
 // rest); 256 accumulator columns need 128 registers a thread, so the other roles
 // give theirs up, down to 104 (at 56 they spill, and the kernel takes 10 to 20 %
@@ -703,8 +703,8 @@ fq_status launch_matmul(const uint8_t *a, int64_t a_rows, const uint8_t *b, int6
 // accumulator is a column of c; a block's products are scaled by the row's scale,
 // which a shuffle hands round.  With few tiles the blocks of K are split over a
 // cluster of S CTAs, whose sums are added through shared memory in rank order.
-// Bound by HBM: 512 rows over 32 experts of 4096 x 7168 in 150 to 160 us, 5.9 to 6.3
-// TB/s; one row through 14336 x 4096 in 15.3 us, 3.8 TB/s, of which the launch, the
+// Bound by HBM: 512 rows over 32 experts of 4096 x 7168 in 152 to 163 us, 5.8 to 6.2
+// TB/s; one row through 14336 x 4096 in 15.6 us, 3.8 TB/s, of which the launch, the
 // set-up and the first and last bytes' latency are about 6 us.
 template <int kT>
 struct Few {
@@ -1050,7 +1050,7 @@ fq_status launch_forward(const uint8_t *a, const uint8_t *b, int64_t K, const Mm
 // byte where M % 16 != 0, and the groups at any token: neither is a tensor
 // copy's alignment.  A lane makes 16 bytes of kAlignRun consecutive blocks, each
 // from five aligned words.  Bound by HBM (every byte read and written once): 65536
-// tokens x 9216 rows in 209 us, 6.0 TB/s; a block at a time, with a division and a
+// tokens x 9216 rows in 212 us, 5.7 TB/s; a block at a time, with a division and a
 // search each, took 325 us.
 constexpr int kAlignRun = 4;
 __global__ void __launch_bounds__(kThreads) align_blocks_kernel(

@@ -115,7 +115,7 @@ __device__ __forceinline__ void load_logits(const void *logits, int64_t row, int
 // One warp per token; lane l holds the kVals experts from kVals l on, so that ties
 // of the warp's largest key go to the lowest lane: one maximum and one ballot a
 // choice.  A lane's keys are sorted once in runs of four (stable), and the choices
-// look at the runs' heads only.  Bound by the integer pipe (80 % busy; about 700
+// look at the runs' heads only.  Bound by the integer pipe (75 % busy; about 680
 // instructions a token), not by memory: 16384 x 256 BF16 logits (8.4 MB), k = 8, in
 // 14.0 us; FP32, sigmoid, bias, the best 4 of 8 groups 26 us, 8 tokens of it 4.8.
 // With every lane's keys looked through in each round, and the experts strided over
