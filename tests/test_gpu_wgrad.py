@@ -228,3 +228,42 @@ def test_same_bits_on_another_stream(fq):
         other = fq.fp8_matmul_wgrad(a, sa, b, sb)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(first, other)
+
+
+STARTS = [  # M, offsets of nine groups
+    (1024, [0, 1, 16, 17, 145, 272, 400, 415, 900, 1023]),
+    (1024, [0, 3, 131, 260, 388, 388, 401, 657, 658, 1024]),
+    (1040, [0, 128, 256, 259, 264, 266, 300, 428, 1000, 1040]),
+    (16, [0, 0, 0, 5, 5, 6, 15, 16, 16, 16]),
+    (2048, [0, 134, 263, 392, 522, 680, 937, 1193, 1462, 2047]),
+]
+
+
+@pytest.mark.parametrize("M,starts", STARTS)
+@pytest.mark.parametrize("N,K", [(1, 1), (130, 264), (500, 1020)])
+def test_wgrad_of_groups_from_any_token(fq, M, starts, N, K):
+    """Rows of M % 16 == 0 tokens, groups that start at any byte of them, tiles of
+    one CTA and of a pair.  A group of NaN codes must not be seen in the others."""
+    offs = np.array(starts)
+    G = len(offs) - 1
+    gen = torch.Generator(device="cuda").manual_seed(M + N)
+    cap = fq.fp4_to_fp8_cols_scale_capacity(M, G)
+    a, sa = operands(M, N, offs, gen, cap)
+    b, sb = operands(M, K, offs, gen, cap)
+    dev = torch.from_numpy(offs).cuda()
+    ref, mag, blocks = reference(a, sa, b, sb, offs)
+    for dtype in (torch.float32, torch.bfloat16):
+        out = fq.fp8_matmul_wgrad(a, sa, b, sb, dev, out_dtype=dtype)
+        check(out, ref, mag, blocks)
+        before = torch.randn((G, N, K), device="cuda", generator=gen).to(dtype)
+        again = fq.fp8_matmul_wgrad(a, sa, b, sb, dev, out=before.clone(), accumulate=True)
+        check(again, ref, mag, blocks, before)
+    plain = fq.fp8_matmul_wgrad(a, sa, b, sb, dev)
+    for g in (4, 7):
+        x, y = a.clone(), b.clone()
+        x[:, int(offs[g]):int(offs[g + 1])] = 0x7F
+        y[:, int(offs[g]):int(offs[g + 1])] = 0xFF
+        out = fq.fp8_matmul_wgrad(x, sa, y, sb, dev)
+        keep = [i for i in range(G) if i != g]
+        assert torch.equal(out[keep], plain[keep])
+        assert bool(out[g].isnan().all()) == bool(offs[g + 1] > offs[g])
