@@ -10,13 +10,13 @@
 //   a block holding NaN or Inf gets s = NaN and codes 0x7F.
 //
 // 2 bytes read and 1 written per element, 4 bytes written per block and feature:
-// 65536 x 2048 in 32 ragged groups in 78 us, 5.2 TB/s.  HBM and the instructions
+// 65536 x 2048 in 32 ragged groups in 73 us, 5.6 TB/s.  HBM and the instructions
 // share the bound.  8 CTAs of 128 threads per SM, a tile of 64 features, the next
 // tile's values fetched while the last is written out; 4 CTAs of 256 threads and 128
-// features: 82 us, without the early fetch 86, 5 of those CTAs 83 to 87.  Blocks of
-// fewer than 128 tokens in 16-byte pieces too: 256 groups of about 64 tokens, 16384 x
-// 7168: 147 us, byte by byte 169.  Written as 4-byte words, a warp a row, 65536 x 2048
-// took 172 us; with the divisions in every thread 94.
+// features 5 % more, without the early fetch 10 %.  Blocks of fewer than 128 tokens in
+// 16-byte pieces too: 256 groups of about 64 tokens, 16384 x 7168: 143 us, byte by
+// byte 165.  Written as 4-byte words, a warp a row, 65536 x 2048 took 172 us; with the
+// divisions in every thread 94.
 #include <cfloat>
 
 #include "fq_tc.cuh"
@@ -29,11 +29,13 @@ constexpr int kTok = 128;   // tokens of a block
 constexpr int kFeat = 64;   // features of a tile
 constexpr int kColThreads = 128;
 
-// Byte of (feature, token) of a tile in shared memory: rows of 128 tokens,
-// 16 bytes further after every 8 features.  A half-warp storing twice 8 tokens of 8
-// features 8 apart then touches 16 different 8-byte bank pairs.
-__device__ __forceinline__ int tile_byte(int f, int t) { return f * kTok + (f >> 3) * 16 + t; }
-constexpr int kTileBytes = kFeat * kTok + (kFeat / 8) * 16 + 16;
+// Byte of (feature, token) of a tile in shared memory: rows of 128 tokens and 8
+// bytes, 80 bytes further after every 8 features.  A half-warp storing twice 8 tokens
+// of 8 features 8 apart then touches 16 different 8-byte bank pairs, and a warp reading
+// words 16 bytes apart of four rows meets every bank twice (rows of 128 bytes: four
+// times, 78 us).
+__device__ __forceinline__ int tile_byte(int f, int t) { return f * (kTok + 8) + (f >> 3) * 80 + t; }
+constexpr int kTileBytes = kFeat * (kTok + 8) + (kFeat / 8) * 80 + 16;
 
 __device__ __forceinline__ uint32_t cvt_e4m3_pair(float lo, float hi)
 {
