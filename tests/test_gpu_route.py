@@ -116,6 +116,10 @@ def test_ties_go_to_the_lowest_index(fq):
         assert ids.tolist() == [[0, 1], [40, 41], [0, 7]]
 
 
+# a second name, as the first is bound to another test further down
+test_equal_logits_go_to_the_lowest_index = test_ties_go_to_the_lowest_index
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_masks(fq, dtype, score):
