@@ -10,9 +10,10 @@
 //          `keep` groups with the largest sum of their best `top` choices
 //   ids    the k largest choices, ties to the lowest index
 //   weight w_j = scale * s_j, or scale * s_j / (sum of the chosen s)
-// in binary32.  A logit that is NaN or at or below BF16's lowest finite value
-// masks its expert: never chosen, score 0.  A slot without an expert (fewer
-// than k available) gets id -1 and weight 0.
+// in binary32; the quotients of softmax scores relative to the largest chosen one,
+// so that they hold where the scores themselves underflow.  A logit that is NaN or
+// at or below BF16's lowest finite value masks its expert: never chosen, score 0.
+// A slot without an expert (fewer than k available) gets id -1 and weight 0.
 #include <cfloat>
 #include <cmath>
 
@@ -63,6 +64,12 @@ __device__ __forceinline__ float warp_sum(float v)
     for (int d = 16; d > 0; d >>= 1)
         v += __shfl_xor_sync(kFull, v, d);
     return v;
+}
+
+// Largest of the warp's values, none of them NaN.
+__device__ __forceinline__ float warp_max(float v)
+{
+    return key_value(__reduce_max_sync(kFull, order_key(v)));
 }
 
 // Largest key of the warp and the lowest lane that has it; 0 if none.
@@ -277,11 +284,14 @@ __global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 2) moe_route_kernel
                     place[q] >>= 8;
                 }
         }
-        float w = 0.0f;
-        if (id >= 0) {
-            const float v = fminf(load_logit<kBf16>(p.logits, row + id), FLT_MAX);
-            w = kSigmoid ? sigmoid_score(v) : expf(v - mx);
-        }
+        float w = 0.0f, v = -INFINITY;
+        if (id >= 0)
+            v = fminf(load_logit<kBf16>(p.logits, row + id), FLT_MAX);
+        // normalised: relative to the largest of the chosen, as in the backward pass;
+        // a bias may choose far below the row's largest, where the scores underflow
+        const float top = kNorm && !kSigmoid ? warp_max(v) : mx;
+        if (id >= 0)
+            w = kSigmoid ? sigmoid_score(v) : expf(v - top);
         if (kNorm)
             sum = warp_sum(w);
         if (kNorm || !kSigmoid)
