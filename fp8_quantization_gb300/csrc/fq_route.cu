@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads) moe_route_backward_kernel(const Rout
                 const float mean = sum > 0.0f ? __fdiv_rn(warp_sum(dw * s), sum) : 0.0f;
                 ds = sum > 0.0f ? __fdiv_rn(dw - mean, sum) : 0.0f;
             }
-            d = ds * s * (1.0f - s);
+            d = ds * s * sigmoid_score(-l);  // 1 - s would cancel where s is next to 1
         } else {
             if (id >= 0)
                 mx = l;

@@ -136,3 +136,19 @@ def test_far_weights_against_differences(fq, score):
             side.append((w * dw).sum(1).double())
         diff = (side[0] - side[1]) / (2 * h)
         assert float((diff - d[:, e].double()).abs().max()) <= tol
+
+
+@pytest.mark.parametrize("spread", [15.0, 30.0, 80.0])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E,k", [(5, 2), (64, 8), (200, 32)])
+def test_sigmoid_gradient_of_scores_next_to_one(fq, spread, dtype, renorm, E, k):
+    """s (1 - s) has to keep its relative accuracy where s rounds to 1."""
+    gen = torch.Generator(device="cuda").manual_seed(E)
+    logits = ((torch.rand((50, E), device="cuda", generator=gen) * 2 - 1) * spread).to(dtype)
+    ids = torch.stack([torch.randperm(E, device="cuda", generator=gen)[:k] for _ in range(50)]).int()
+    # the chosen within 45 of each other (a renormalised weight's range)
+    logits.scatter_(1, ids.long(), logits.gather(1, ids.long()).clamp(min=spread - 45))
+    dw = torch.randn((50, k), device="cuda", generator=gen)
+    d = fq.moe_route_backward(logits, ids, dw, score="sigmoid", renormalize=renorm, scale=2.5)
+    close(d, *gradient64(logits, ids, dw, "sigmoid", renorm, 2.5))
