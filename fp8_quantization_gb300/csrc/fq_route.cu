@@ -10,10 +10,10 @@
 //          `keep` groups with the largest sum of their best `top` choices
 //   ids    the k largest choices, ties to the lowest index
 //   weight w_j = scale * s_j, or scale * s_j / (sum of the chosen s)
-// in binary32; the quotients of softmax scores relative to the largest chosen one,
-// so that they hold where the scores themselves underflow.  A logit that is NaN or
-// at or below BF16's lowest finite value masks its expert: never chosen, score 0.
-// A slot without an expert (fewer than k available) gets id -1 and weight 0.
+// in binary32; the quotients relative to the largest chosen score, so that they
+// hold where the scores themselves underflow.  A logit that is NaN or at or below
+// BF16's lowest finite value masks its expert: never chosen, score 0.  A slot
+// without an expert (fewer than k available) gets id -1 and weight 0.
 #include <cfloat>
 #include <cmath>
 
@@ -70,6 +70,18 @@ __device__ __forceinline__ float warp_sum(float v)
 __device__ __forceinline__ float warp_max(float v)
 {
     return key_value(__reduce_max_sync(kFull, order_key(v)));
+}
+
+// The score of logit l (at most `top`) up to a factor of the row, so that the largest
+// is 1/2 or more: exp(l - top), or the sigmoid exp(l) / (1 + exp(l)) times exp(-top)
+// where top < 0.
+template <bool kSigmoid>
+__device__ __forceinline__ float relative_score(float l, float top)
+{
+    if (!kSigmoid)
+        return expf(l - top);
+    const float e = expf(-fabsf(l));
+    return __fdiv_rn(l < 0.0f ? expf(l - fminf(top, 0.0f)) : 1.0f, 1.0f + e);
 }
 
 // Largest key of the warp and the lowest lane that has it; 0 if none.
@@ -289,9 +301,9 @@ __global__ void __launch_bounds__(kThreads, kVals <= 8 ? 4 : 2) moe_route_kernel
             v = fminf(load_logit<kBf16>(p.logits, row + id), FLT_MAX);
         // normalised: relative to the largest of the chosen, as in the backward pass;
         // a bias may choose far below the row's largest, where the scores underflow
-        const float top = kNorm && !kSigmoid ? warp_max(v) : mx;
+        const float top = kNorm ? warp_max(v) : mx;
         if (id >= 0)
-            w = kSigmoid ? sigmoid_score(v) : expf(v - top);
+            w = kNorm ? relative_score<kSigmoid>(v, top) : kSigmoid ? sigmoid_score(v) : expf(v - top);
         if (kNorm)
             sum = warp_sum(w);
         if (kNorm || !kSigmoid)
@@ -329,7 +341,8 @@ __device__ __forceinline__ void store_grad(void *dl, int64_t at, float v, bool b
 // With q_j = s_j / sum of the chosen s (normalised) the
 // gradient of a chosen score is ds_j = scale (dw_j - sum_i dw_i q_i) / sum;
 // through the softmax that is dl_j = scale q_j (dw_j - sum_i dw_i q_i) and 0
-// elsewhere, which needs the chosen logits only.  Not normalised, softmax:
+// elsewhere, through the sigmoid that times 1 - s_j: the chosen logits are enough,
+// and nothing is divided by a sum that may underflow.  Not normalised, softmax:
 // dl_e = p_e (ds_e - sum_j ds_j p_j) for every expert.
 template <bool kBf16, bool kSigmoid, bool kNorm>
 __global__ void __launch_bounds__(kThreads) moe_route_backward_kernel(const RouteGradArgs p)
@@ -353,14 +366,19 @@ __global__ void __launch_bounds__(kThreads) moe_route_backward_kernel(const Rout
         float d = 0.0f, rest = 0.0f;  // gradient of the slot's logit; of another logit: -rest * p_e
         float mx = -FLT_MAX, inv = 0.0f;
         if (kSigmoid) {
-            const float s = id >= 0 ? sigmoid_score(l) : 0.0f;
-            float ds = dw;
+            // 1 - s as the sigmoid of -l: the difference would cancel next to s = 1
+            const float e = expf(-fabsf(l)), large = __fdiv_rn(1.0f, 1.0f + e), small = e * large;
+            const float slope = l < 0.0f ? large : small;
+            float q = l < 0.0f ? small : large, mean = 0.0f;  // q: the weight without `scale`
             if (kNorm) {
-                const float sum = warp_sum(s);
-                const float mean = sum > 0.0f ? __fdiv_rn(warp_sum(dw * s), sum) : 0.0f;
-                ds = sum > 0.0f ? __fdiv_rn(dw - mean, sum) : 0.0f;
+                const float top = fminf(warp_max(l), 0.0f);
+                if (l < 0.0f)
+                    q = id >= 0 ? expf(l - top) * large : 0.0f;
+                const float sum = warp_sum(q);
+                q = sum > 0.0f ? __fdiv_rn(q, sum) : 0.0f;
+                mean = warp_sum(dw * q);
             }
-            d = ds * s * sigmoid_score(-l);  // 1 - s would cancel where s is next to 1
+            d = q * (dw - mean) * slope;
         } else {
             if (id >= 0)
                 mx = l;

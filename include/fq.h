@@ -311,9 +311,8 @@ fq_status fp8_matmul_wgrad(const uint8_t *aT, const float *aT_scale, int64_t N, 
  *          experts it has), and only the keep_groups best runs are open
  *   ids    : int32 [T, k] (output) the k largest choices, largest first
  *   weights: float [T, k] (output) scale * s of each, divided by the sum of the
- *          k scores if renormalize = 1 (softmax: relative to the largest of them,
- *          so that the quotient holds where the scores underflow; sigmoid: 0
- *          where that sum is 0)
+ *          k scores if renormalize = 1 (relative to the largest of them, so that
+ *          the quotient holds where the scores themselves underflow)
  * All in binary32; ties go to the lowest index.  Without a bias, softmax
  * scores are compared before their division by the row's sum.  An expert
  * whose logit is NaN or at or below BF16's lowest finite value (-0x1.FEp127:

@@ -109,7 +109,7 @@ def test_softmax_weights_below_the_largest_logit_of_a_closed_group(fq):
     assert bool(((w.double() - ref).abs() <= REL * ref).all())
 
 
-@pytest.mark.parametrize("score", ["softmax"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_far_weights_against_differences(fq, score):
     """Central differences of the kernel's own weights, 95 to 100 below the leading
     logit (softmax) or at -100 to -95 (sigmoid): the backward pass is the derivative
@@ -152,3 +152,20 @@ def test_sigmoid_gradient_of_scores_next_to_one(fq, spread, dtype, renorm, E, k)
     dw = torch.randn((50, k), device="cuda", generator=gen)
     d = fq.moe_route_backward(logits, ids, dw, score="sigmoid", renormalize=renorm, scale=2.5)
     close(d, *gradient64(logits, ids, dw, "sigmoid", renorm, 2.5))
+
+
+@pytest.mark.parametrize("low,high", [(-100.0, -60.0), (-90.0, -80.0), (-145.0, -105.0), (-30.0, 15.0)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,k", [(9, 1), (33, 4), (256, 8)])
+def test_sigmoid_weights_of_tiny_scores(fq, low, high, dtype, E, k):
+    """Renormalised weights are quotients of scores that may lie below binary32's
+    numbers; the gradient is of the size of dweights, which is large here."""
+    logits, bias, gen = far_below(40, E, low, high, dtype, E)
+    w, ids = fq.moe_route(logits, k, bias=bias, score="sigmoid", scale=2.5)
+    if high < -20:  # the scores do not move the choice
+        assert torch.equal(ids, torch.argsort(bias, descending=True)[:k].int().expand(40, k))
+    ref = weights64(logits, ids, "sigmoid", 2.5)
+    assert bool(((w.double() - ref).abs() <= REL * ref).all())
+    dw = 3000.0 * torch.randn((40, k), device="cuda", generator=gen)
+    d = fq.moe_route_backward(logits, ids, dw, score="sigmoid", scale=2.5)
+    close(d, *gradient64(logits, ids, dw, "sigmoid", True, 2.5))
