@@ -343,7 +343,8 @@ __device__ __forceinline__ void store_grad(void *dl, int64_t at, float v, bool b
 // through the softmax that is dl_j = scale q_j (dw_j - sum_i dw_i q_i) and 0
 // elsewhere, through the sigmoid that times 1 - s_j: the chosen logits are enough,
 // and nothing is divided by a sum that may underflow.  Not normalised, softmax:
-// dl_e = p_e (ds_e - sum_j ds_j p_j) for every expert.
+// dl_e = p_e (ds_e - sum_j ds_j p_j) for every expert.  An id that stands in several
+// slots has the sum of their gradients.
 template <bool kBf16, bool kSigmoid, bool kNorm>
 __global__ void __launch_bounds__(kThreads) moe_route_backward_kernel(const RouteGradArgs p)
 {
@@ -357,6 +358,8 @@ __global__ void __launch_bounds__(kThreads) moe_route_backward_kernel(const Rout
         float l = -INFINITY, dw = 0.0f;
         if (id >= 0 && id < p.E)
             l = load_logit<kBf16>(p.logits, row + id);
+        const unsigned same = __match_any_sync(kFull, id);  // while the logit is on its way
+        const bool repeated = __any_sync(kFull, id >= 0 && (same & (same - 1)) != 0);
         if (l > kMasked) {
             l = fminf(l, FLT_MAX);
             dw = __ldg(p.dw + t * p.k + lane) * p.scale;
@@ -415,6 +418,19 @@ __global__ void __launch_bounds__(kThreads) moe_route_backward_kernel(const Rout
                     v = -rest * (expf(fminf(x, FLT_MAX) - mx) * inv);
             }
             store_grad(p.dl, row + e, v, kBf16);
+        }
+        if (repeated) {  // the first slot's lane takes the sum, in slot order
+            constexpr bool kRow = !kSigmoid && !kNorm;  // `rest` counts once for a logit
+            const float part = kRow ? dw : d;
+            float total = 0.0f;
+            for (int j = 0; j < p.k; j++) {
+                const float v = __shfl_sync(kFull, part, j);
+                if ((same >> j) & 1u)
+                    total += v;
+            }
+            d = kRow ? expf(l - mx) * inv * (total - rest) : total;
+            if (lane != __ffs(same) - 1)
+                id = -1;
         }
         __syncwarp();  // the chosen logits' gradients go over the row
         if (id >= 0)

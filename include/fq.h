@@ -329,7 +329,8 @@ fq_status moe_route(const void *logits, int logits_f32, int64_t T, int32_t E, in
 
 /*
  * Gradient of moe_route's weights with respect to the logits, for the ids it
- * chose (which are constants; an id outside [0, E) takes no part).
+ * chose (which are constants; an id outside [0, E) takes no part, and the
+ * gradients of slots with the same id are added in slot order).
  *   dweights : float [T, k];  dlogits : [T, E] in the logits' type (output)
  * logits, sigmoid, renormalize and scale as given to moe_route.
  */

@@ -169,3 +169,21 @@ def test_sigmoid_weights_of_tiny_scores(fq, low, high, dtype, E, k):
     dw = 3000.0 * torch.randn((40, k), device="cuda", generator=gen)
     d = fq.moe_route_backward(logits, ids, dw, score="sigmoid", scale=2.5)
     close(d, *gradient64(logits, ids, dw, "sigmoid", True, 2.5))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,k", [(3, 3), (40, 6), (40, 32), (300, 8)])
+def test_gradients_of_an_id_that_stands_twice_are_added(fq, score, renorm, dtype, E, k):
+    """Ids drawn with repetition, some without an expert: every slot's gradient
+    counts, and the bits are the same each time."""
+    gen = torch.Generator(device="cuda").manual_seed(E + k)
+    logits = (torch.rand((60, E), device="cuda", generator=gen) * 10 - 5).to(dtype)
+    ids = torch.randint(-1, min(E, 7), (60, k), device="cuda", generator=gen, dtype=torch.int32)
+    ids[0] = 2
+    dw = torch.randn((60, k), device="cuda", generator=gen)
+    d = fq.moe_route_backward(logits, ids, dw, score=score, renormalize=renorm, scale=2.5)
+    close(d, *gradient64(logits, ids, dw, score, renorm, 2.5))
+    again = fq.moe_route_backward(logits, ids, dw, score=score, renormalize=renorm, scale=2.5)
+    assert torch.equal(d, again)
