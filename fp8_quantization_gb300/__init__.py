@@ -549,7 +549,7 @@ def fp8_matmul_wgrad(aT: torch.Tensor, aT_scale: torch.Tensor, bT: torch.Tensor,
     dt = _out_dtype(out, out_dtype)
     out = _out(out, (G, N, K), dt, aT, "out")
     need = fp8_matmul_wgrad_workspace(M, N, K, G)
-    if group_offsets is None and M % 16 == 0 and M > 0:
+    if group_offsets is None and M % 16 == 0:
         need = 0  # read in place
     if workspace is None and need > 0:
         workspace = _empty((need,), torch.uint8, aT)

@@ -1211,7 +1211,7 @@ extern "C" fq_status fp8_matmul_wgrad(const uint8_t *aT, const float *aT_scale, 
         return FQ_ERR_SHAPE;
     // one group from token 0 on, rows of M tokens 16-byte aligned: the blocks lie
     // where tensor copies can fetch them
-    const bool in_place = !group_offsets && M % 16 == 0 && M > 0;
+    const bool in_place = !group_offsets && M % 16 == 0;
     if (cap < fp4_to_fp8_cols_scale_capacity(M, G) || (!in_place && workspace_bytes < need))
         return FQ_ERR_ARG;
     if ((M > 0 && (!aT || !aT_scale || !bT || !bT_scale)) || !c || (!in_place && !workspace))
@@ -1222,7 +1222,11 @@ extern "C" fq_status fp8_matmul_wgrad(const uint8_t *aT, const float *aT_scale, 
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const uint8_t *wa = aT, *wb = bT;
     int64_t pitch = M;
-    if (!in_place) {
+    if (in_place && M == 0) {
+        // no blocks, so no copies: the maps need an address and a size, not operands
+        wa = wb = static_cast<const uint8_t *>(c);
+        pitch = 128;
+    } else if (!in_place) {
         const int64_t blocks = fp4_to_fp8_cols_scale_capacity(M, G);
         pitch = 128 * blocks;
         uint8_t *ws = static_cast<uint8_t *>(workspace);
