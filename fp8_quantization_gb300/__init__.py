@@ -123,6 +123,14 @@ def _p(t: torch.Tensor | None) -> int:
     return 0 if t is None else t.data_ptr()
 
 
+def _int32(v, name: str) -> int:
+    """A count that the C ABI takes as int32 (ctypes would cut it to 32 bits)."""
+    n = int(v)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {v}")
+    return n
+
+
 def _need(t: torch.Tensor, dtype, name: str, ndim: int | None = None,
           numel: int | None = None, shape: tuple | None = None):
     """dtype, contiguity and size of a tensor argument (placement is checked
@@ -520,6 +528,8 @@ def fp8_quantize_cols(x: torch.Tensor, group_offsets: torch.Tensor | None = None
 
 def fp8_matmul_wgrad_workspace(M: int, N: int, K: int, G: int) -> int:
     """Bytes of workspace fp8_matmul_wgrad needs (-1 for a rejected shape)."""
+    if not 1 <= G <= FQ_COLS_MAX_GROUPS:
+        return -1
     return int((_lib or abi()).fp8_matmul_wgrad_workspace(int(M), int(N), int(K), int(G)))
 
 
@@ -588,13 +598,15 @@ def moe_route(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None,
     runs of experts, weights divided by their sum if `renormalize`, times
     `scale`.  A slot without an available expert has id -1 and weight 0."""
     T, E = _logits(logits, score)
+    k, n_groups = _int32(k, "k"), _int32(n_groups, "n_groups")
+    keep_groups, group_top = _int32(keep_groups, "keep_groups"), _int32(group_top, "group_top")
     weights = _out(weights, (T, k), torch.float32, logits, "weights")
     ids = _out(ids, (T, k), torch.int32, logits, "ids")
     if bias is not None:
         _need(bias, torch.float32, "bias", numel=E)
     _on_device(logits=logits, bias=bias, weights=weights, ids=ids)
-    _call("moe_route", _p(logits), int(logits.dtype == torch.float32), T, E, int(k), _p(bias),
-          int(score == "sigmoid"), int(n_groups), int(keep_groups), int(group_top),
+    _call("moe_route", _p(logits), int(logits.dtype == torch.float32), T, E, k, _p(bias),
+          int(score == "sigmoid"), n_groups, keep_groups, group_top,
           int(bool(renormalize)), float(scale), _p(weights), _p(ids), _stream())
     return weights, ids
 
@@ -619,6 +631,8 @@ def moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.
 
 def moe_sort_rows_workspace(n: int, n_experts: int) -> int:
     """Bytes of workspace moe_sort_rows needs for n pairs (-1: rejected)."""
+    if not 1 <= n_experts <= FQ_COLS_MAX_GROUPS:
+        return -1
     return int((_lib or abi()).moe_sort_rows_workspace(int(n), int(n_experts)))
 
 
@@ -631,7 +645,7 @@ def moe_sort_rows(ids: torch.Tensor, n_experts: int, group_offsets: torch.Tensor
     choice) pairs ordered by expert, and within an expert by index.  Row r
     holds token pair_of_row[r] // k; ids outside [0, E) get no row (-1)."""
     _need(ids, torch.int32, "ids")
-    n, E = ids.numel(), int(n_experts)
+    n, E = ids.numel(), _int32(n_experts, "n_experts")
     group_offsets = _out(group_offsets, (max(E, 0) + 1,), torch.int64, ids, "group_offsets")
     pair_of_row = _out(pair_of_row, (n,), torch.int32, ids, "pair_of_row")
     row_of_pair = _out(row_of_pair, tuple(ids.shape), torch.int32, ids, "row_of_pair")
