@@ -136,7 +136,7 @@ __device__ __forceinline__ void load_logits(const void *logits, int64_t row, int
 // choice.  A lane's keys are sorted once in runs of four (stable), and the choices
 // look at the runs' heads only.  Bound by the integer pipe (75 % busy; about 680
 // instructions a token), not by memory: 16384 x 256 BF16 logits (8.4 MB), k = 8, in
-// 14.0 us; FP32, sigmoid, bias, the best 4 of 8 groups 26 us, 8 tokens of it 4.8.
+// 14.25 us; FP32, sigmoid, bias, the best 4 of 8 groups 26.7 us, 8 tokens of it 4.9.
 // With every lane's keys looked through in each round, and the experts strided over
 // the lanes (a second reduction for ties): 18.1, 46 and 6.5 us.  Left to itself the
 // compiler keeps the registers at 48 to 128 and spills: 1000 experts 53 us for 43.
@@ -337,7 +337,10 @@ __device__ __forceinline__ void store_grad(void *dl, int64_t at, float v, bool b
         static_cast<float *>(dl)[at] = v;
 }
 
-// One warp per token; bound by the writing of dlogits: 16384 x 256 BF16 in 7.7 us.
+// One warp per token.  Bound by latency (ids, their logits, reductions over the warp;
+// memory 22 % busy): 16384 x 256 BF16 in 4.5 us out of the L2 and 7.4 us alone, 65536 x
+// 256 19.9 us; FP32 sigmoid 5.45 us; not normalised, which reads the row three times,
+// 10.5 us.
 // With q_j = s_j / sum of the chosen s (normalised) the
 // gradient of a chosen score is ds_j = scale (dw_j - sum_i dw_i q_i) / sum;
 // through the softmax that is dl_j = scale q_j (dw_j - sum_i dw_i q_i) and 0

@@ -230,7 +230,8 @@ fq_status fp8_quantize_128x128(const void *w, int64_t N, int64_t K, uint8_t *y, 
  *   c[m, n] = sum over the blocks t of K of  sa[m, t] sb[g, n, t] *
  *             sum over k in t of  a[m, k] b[g, n, k]
  * with the inner and the outer sum in binary32, rounded once to BF16 where
- * c is BF16.  A NaN scale or code makes the outputs that it enters NaN.
+ * c is BF16; scale products and scaled block sums have to stay in its range.
+ * A NaN scale or code makes the outputs that it enters NaN.
  * Rows offsets[G] .. M-1, which belong to no group, are written as 0.
  * Forward: a = activations, b = weights; input gradient: a = output
  * gradients, b = the codes and scales of the transposed weights.
@@ -278,11 +279,13 @@ fq_status fp8_quantize_cols(const void *x, int64_t M, int64_t K, const int64_t *
  *   c[g, n, k] = sum over the 128-token blocks b of group g of
  *                aT_scale[b, n] bT_scale[b, k] *
  *                sum over tokens t in b of  aT[n, t] bT[k, t]
- * sums in binary32, rounded once.  An empty group's gradient is 0.
+ * sums in binary32, rounded once (scaled block sums have to stay in its range).
+ * An empty group's gradient is 0.
  * accumulate = 1 adds to what c holds instead (an empty group's stays).
  *   workspace : device memory of at least fp8_matmul_wgrad_workspace(M, N, K,
  *        G) bytes (-1 for a rejected shape), 16-byte aligned, overwritten; the
- *        operands are re-laid there block by block.  Not used, and may be NULL
+ *        operands are re-laid there block by block, so it is as large as both of
+ *        them with each group filled up to whole blocks.  Not used, and may be NULL
  *        and 0, where group_offsets is NULL and M % 16 == 0.
  *   dev_status : as in fp8_matmul
  * Requires N, K > 0 (K % 8 == 0 stores 16 bytes at a time), 1 <= G <=
