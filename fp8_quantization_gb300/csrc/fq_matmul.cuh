@@ -1428,6 +1428,12 @@ fq_status launch_matmul(const uint8_t *a, int64_t a_rows, const uint8_t *b, int6
 // TB/s; one row through 14336 x 4096 in 15.6 us, 3.8 TB/s, of which the launch, the
 // set-up and the first and last bytes' latency are about 6 us.
 // Gated: a stage holds 128 gate rows and the up rows beside them, a lane both sums.
+// Two CTAs share an SM up to 480 groups, whose offsets lie behind the stages (a quantized
+// gated result by tiles of 32 rows: 371, for the magnitudes beside them; up to 1024 with the
+// tiles of 32 and 64 rows that are not gated, or of 16 gated).  Above, one does: 4 rows in
+// each of 464 groups of 512 x 2048 84 us with two, 88 with one; with 512 groups a stage fewer
+// for two instead of one took 94.2 for 93.7, 12 rows in each 100.4 for 98.4, and gated by
+// tiles of 32 rows 187 for 194.
 template <int kT, bool kGatedTile>
 struct Few {
     // CTAs per SM and their stages: about 200 KB of weights in flight per SM
@@ -1439,19 +1445,34 @@ struct Few {
     static constexpr int threads = 6 * 32;
 };
 
-template <int kT, bool kGatedTile>
-struct FewTail {
+// Largest magnitudes of a block: of every row of a by every warp.
+template <int kT, bool kQuantized>
+struct FewMax {
+    uint32_t row_max[2][4][kT];
+};
+template <int kT>
+struct FewMax<kT, false> {};
+
+template <int kT, bool kGatedTile, bool kQuantized>
+struct FewTail : FewMax<kT, kQuantized> {
     using F = Few<kT, kGatedTile>;
     uint64_t full[F::stages], empty[F::stages];
     uint64_t acc_full[F::bufs], acc_empty[F::bufs];
     uint32_t tmem;
     int32_t abort;
-    // largest magnitudes of a block: of every row of a by every warp
-    uint32_t row_max[kGatedTile ? 2 : 1][4][kT];
     // int32 off[G + 2], first[G + 2] follow
 };
 
-// Warps 0-3 add up the blocks, warp 4 issues the tensor copies, warp 5 the MMAs.
+// Bytes of shared memory that a CTA is launched with; two CTAs share an SM with 113 KB each.
+template <int kT, bool kGatedTile, bool kQuantized>
+constexpr int few_bytes(int32_t G)
+{
+    using F = Few<kT, kGatedTile>;
+    return 1024 + F::stages * (F::w_bytes + F::x_bytes) +
+           static_cast<int>(sizeof(FewTail<kT, kGatedTile, kQuantized>)) +
+           2 * (G + 2) * static_cast<int>(sizeof(int32_t));
+}
+
 // The end of a tile of few rows: what a lane makes of the sums of column n, two rows at a
 // time (the second of them may be missing).  The form of the activation is chosen once a
 // tile: with a branch a row, 8192 x 512 x 2048 in 256 groups took 97 us with bias, silu,
@@ -1554,6 +1575,7 @@ struct FewFinish {
     }
 };
 
+// Warps 0-3 add up the blocks, warp 4 issues the tensor copies, warp 5 the MMAs.
 template <int kT, Mode kMode, Out kOut, Epi kEpi>
 __global__ void __launch_bounds__(Few<kT, kEpi == kGated>::threads, Few<kT, kEpi == kGated>::per_sm)
     fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw,
@@ -1565,7 +1587,7 @@ __global__ void __launch_bounds__(Few<kT, kEpi == kGated>::threads, Few<kT, kEpi
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sW = smem, *sX = sW + F::stages * F::w_bytes;
-    using Tail = FewTail<kT, kGatedTile>;
+    using Tail = FewTail<kT, kGatedTile, kOut == kE4m3>;
     Tail &t = *reinterpret_cast<Tail *>(sX + F::stages * F::x_bytes);
     int32_t *off = reinterpret_cast<int32_t *>(&t + 1), *first = off + p.G + 2;
     volatile int32_t *abort = &t.abort;
@@ -1991,8 +2013,10 @@ fq_status launch_few(const uint8_t *a, const uint8_t *b, int64_t K, const MmArgs
         return FQ_ERR_CUDA;
     }
     const auto kern = fp8_matmul_few_kernel<kT, kMode, kOut, kEpi>;
-    const size_t dyn = 1024 + F::stages * (F::w_bytes + F::x_bytes) + sizeof(FewTail<kT, kEpi == kGated>) +
-                       2 * (p.G + 2) * sizeof(int32_t);
+    constexpr bool kQuantized = kOut == kE4m3;
+    static_assert(few_bytes<kT, kEpi == kGated, kQuantized>(kQuantized ? 371 : 480) <= 113 * 1024,
+                  "two CTAs of an SM, as many groups as the comment above says");
+    const size_t dyn = few_bytes<kT, kEpi == kGated, kQuantized>(p.G);
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(dyn)) != cudaSuccess)
         return launch_status();
