@@ -1999,6 +1999,14 @@ int few_split(int64_t tiles, int64_t blocks)
     return S;
 }
 
+// Tiles of kT rows: with one group they are known, otherwise at most so many.
+template <int kT>
+int64_t few_tiles(const MmArgs &p)
+{
+    const int64_t nt = (p.N + 127) / 128;
+    return (p.offs ? p.M / kT + (p.G < p.M ? p.G : p.M) + 1 : (p.M + kT - 1) / kT) * nt;
+}
+
 template <int kT, Mode kMode, Out kOut, Epi kEpi>
 fq_status launch_few(const uint8_t *a, const uint8_t *b, int64_t K, const MmArgs &p, cudaStream_t st)
 {
@@ -2020,10 +2028,7 @@ fq_status launch_few(const uint8_t *a, const uint8_t *b, int64_t K, const MmArgs
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(dyn)) != cudaSuccess)
         return launch_status();
-    const int64_t nt = (p.N + 127) / 128;
-    // with one group the tiles are known, otherwise at most so many
-    const int64_t tiles = (p.offs ? p.M / kT + (p.G < p.M ? p.G : p.M) + 1 : (p.M + kT - 1) / kT) * nt;
-    const int64_t sms = sm_count();
+    const int64_t tiles = few_tiles<kT>(p), sms = sm_count();
     const int S = few_split<kT>(tiles, p.KB);
     const int64_t most = S > 1 ? tiles : F::per_sm * sms;
     cudaLaunchConfig_t cfg = {};
@@ -2065,8 +2070,8 @@ inline bool one_cta_tiles(int64_t rows, int64_t cols, int64_t groups, int percen
 // CTAs of a large tile (1, 2), whichever ends first by its time without blocks, that of
 // a block, and for few rows what more CTAs than SMs add, and each row whose sums come
 // from a cluster's CTAs.  Fitted to the five kernels' times at 200 sizes (1 to 2000 rows, dense
-// and in 4 to 32 groups, x 128 to 4096 columns, K 1024 to 7168): the choice is 0.3 % behind
-// the best of the five on average, 24 % at most.  64 x 2 x 896 x 7168: few rows 9.1 us, one CTA
+// and in 4 to 32 groups, x 128 to 4096 columns, K 1024 to 7168): the choice is 0.7 % behind
+// the best of the five on average, 21 % at most.  64 x 2 x 896 x 7168: few rows 9.1 us, one CTA
 // a tile 27.7; 100 x 1408 x 1024: 6.0, 8.6; 200 x 4096 x 7168: 22.5, 21.9.
 template <Epi kEpi>
 int pick_small(const MmArgs &p)
@@ -2090,7 +2095,8 @@ int pick_small(const MmArgs &p)
     const int64_t mean = (M + p.G - 1) / p.G;
     const auto few = [&](auto rows, int64_t fixed, int64_t block, int64_t many, int64_t row) {
         constexpr int kT = decltype(rows)::value;
-        const int64_t tiles = row_tiles(kT) * nt, S = few_split<kT>(tiles, p.KB);
+        // (split as the launch will split it)
+        const int64_t tiles = row_tiles(kT) * nt, S = few_split<kT>(few_tiles<kT>(p), p.KB);
         const int64_t waves = (tiles * S + 2 * sms - 1) / (2 * sms);
         offer(kT, fixed + (tiles * S > sms ? many : 0) +
                       (S > 1 ? (mean < kT ? mean : kT) / S * row : 0) +

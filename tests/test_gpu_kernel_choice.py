@@ -1,0 +1,30 @@
+"""GPU: products at sizes where the choice between kernels is close, against their 64-bit
+forms within derived bounds (ffn_forms): whichever runs, the result is right."""
+import pytest
+import torch
+
+import ffn_forms as ff
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fq():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import fp8_quantization_gb300 as m
+    m.abi()
+    return m
+
+
+@pytest.mark.parametrize("M,N,K,G", [(64, 1024, 2048, 4), (64, 1024, 1024, 8), (300, 1408, 2048, 7)])
+def test_ragged_rows_whose_k_may_be_split(fq, M, N, K, G):
+    cut = torch.randint(0, M + 1, (G - 1,), generator=torch.Generator().manual_seed(N)).sort().values
+    bounds = [0, *cut.tolist(), M]
+    y, ys, w, ws, gen = ff.make(M, N, K, G, 128, M + N, ())
+    offs = torch.tensor(bounds, device="cuda")
+    x, off = ff.product(y, ys, w, ws, bounds)
+    a, _, da, _ = ff.act(x, "silu")
+    for dtype in (torch.bfloat16, torch.float32):
+        out = fq.fp8_matmul_act(y, ys, w, ws, offs, act="silu", out_dtype=dtype)
+        ff.check("act", out, a, da + ff.SLOPE * off + ff.rounded(a, dtype))
