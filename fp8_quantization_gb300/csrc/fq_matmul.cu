@@ -195,7 +195,7 @@ extern "C" fq_status fp8_matmul_wgrad(const uint8_t *aT, const float *aT_scale, 
     p.R = static_cast<int32_t>(N);
     p.N = static_cast<int32_t>(K);
     p.add = accumulate;
-    if (one_cta_tiles(N, K, G, 104))
+    if (one_cta_tiles(N, K, G, 256, 520))
         return c_f32 ? launch_matmul<1, kWgrad, kF32, kPlain>(wa, N, wb, K, pitch, G * N, p, st)
                      : launch_matmul<1, kWgrad, kBf16, kPlain>(wa, N, wb, K, pitch, G * N, p, st);
     return c_f32 ? launch_matmul<2, kWgrad, kF32, kPlain>(wa, N, wb, K, pitch, G * N, p, st)

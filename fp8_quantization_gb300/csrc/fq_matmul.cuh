@@ -2050,19 +2050,22 @@ fq_status launch_few(const uint8_t *a, const uint8_t *b, int64_t K, const MmArgs
     return launch_status();
 }
 
-// Whether tiles of one CTA (128 x 128) finish before tiles of a pair (256 x 256):
-// rounds over the SMs, a round of pairs counting for two, times `percent` of a
-// pair's time for the same work.  Measured both ways: forward 125 (N x K 4096 x
-// 7168, 512 rows: 128 tiles, one round 21.4 us, pairs 27.0; 1024 rows: 256 tiles, two
-// rounds 37.6, pairs 28.2), weight gradient 104 (1003 tokens, 8 x 1408 x 2048: 10
-// rounds 28.1 us, 6 of pairs 30.9; 16384 tokens, 16 x 2048 x 2048: 27 rounds 150, 14 of
-// pairs 144).
-inline bool one_cta_tiles(int64_t rows, int64_t cols, int64_t groups, int percent)
+// Whether tiles of one CTA (128 x 128) finish before tiles of a pair (256 x pair_cols):
+// rounds over the SMs, a round of one CTA's taking `permille` of a round of pairs.
+// Measured both ways: forward 625 (N x K 4096 x 7168, 512 rows: 128 tiles, one round 21.4
+// us, pairs 27.0; 1024 rows: 256 tiles, two rounds 37.6, pairs 28.2), weight gradient 520
+// (1003 tokens, 8 x 1408 x 2048: 10 rounds 28.1 us, 6 of pairs 30.9; 16384 tokens, 16 x
+// 2048 x 2048: 27 rounds 150, 14 of pairs 144).  Gated, where both kinds of tiles have 128
+// columns of c and a CTA the same work in them, 1170 (384 x 2 x 14336 x 4096: three rounds
+// 58, three of pairs 51; 384 x 2 x 2048 x 20480: one round 82, one of pairs 67; 640 x 2 x
+// 13824 x 5120: four 89, five 93; 896 x 2 x 18944 x 3584: seven 112, eight 111).
+inline bool one_cta_tiles(int64_t rows, int64_t cols, int64_t groups, int64_t pair_cols,
+                          int permille)
 {
     const int64_t sms = sm_count(), pairs = sms > 1 ? sms / 2 : 1;
     const int64_t one = (rows + 127) / 128 * ((cols + 127) / 128) * groups;
-    const int64_t two = (rows + 255) / 256 * ((cols + 255) / 256) * groups;
-    return (one + sms - 1) / sms * percent < (two + pairs - 1) / pairs * 200;
+    const int64_t two = (rows + 255) / 256 * ((cols + pair_cols - 1) / pair_cols) * groups;
+    return (one + sms - 1) / sms * permille < (two + pairs - 1) / pairs * 1000;
 }
 
 // Which kernel an epilogue runs with where the weights are small (up to 64 MB, so
@@ -2159,7 +2162,8 @@ fq_status launch_forward(const uint8_t *a, const uint8_t *b, int64_t K, const Mm
     if constexpr (kEpi != kGated)
         if (mean <= 64 && 2 * nt * p.G <= sms)
             return launch_few<64, kMode, kOut, kEpi>(a, b, K, p, st);
-    if (p.G > 1 ? mean <= 128 : one_cta_tiles(p.M, p.N, 1, 125))
+    if (p.G > 1 ? mean <= 128
+                : one_cta_tiles(p.M, p.N, 1, Shape<2, kOut, kEpi>::step, kEpi == kGated ? 1170 : 625))
         return launch_matmul<1, kMode, kOut, kEpi>(a, p.M, b, b_rows, K, p.M, p, st);
     return launch_matmul<2, kMode, kOut, kEpi>(a, p.M, b, b_rows, K, p.M, p, st);
 }

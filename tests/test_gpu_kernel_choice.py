@@ -28,3 +28,19 @@ def test_ragged_rows_whose_k_may_be_split(fq, M, N, K, G):
     for dtype in (torch.bfloat16, torch.float32):
         out = fq.fp8_matmul_act(y, ys, w, ws, offs, act="silu", out_dtype=dtype)
         ff.check("act", out, a, da + ff.SLOPE * off + ff.rounded(a, dtype))
+
+
+@pytest.mark.parametrize("M,F,K", [(64, 2048, 20480), (384, 2048, 20480), (384, 14336, 4096), (640, 13824, 5120)])
+def test_dense_gated_projections_of_large_weights(fq, M, F, K):
+    """More than 64 MB of weights: tiles of one CTA or of pairs, by their rounds over the SMs."""
+    y, ys, w, ws, _ = ff.make(M, F, K, None, 128, M + F, (2,))
+    gate, dg = ff.product(y, ys, w[0], ws[0])
+    up, du = ff.product(y, ys, w[1], ws[1])
+    a, _, da, _ = ff.act(gate, "silu")
+    da = da + ff.SLOPE * dg
+    want, off = a * up, da * (up.abs() + du) + a.abs() * du
+    z = torch.empty((M, 2, F), dtype=torch.bfloat16, device="cuda")
+    h = fq.fp8_matmul_gated(y, ys, w, ws, z=z, out_dtype=torch.float32)
+    ff.check("h", h, want, off + ff.rounded(want, torch.float32))
+    ff.check("gate", z[:, 0], gate, dg + ff.rounded(gate, torch.bfloat16))
+    ff.check("up", z[:, 1], up, du + ff.rounded(up, torch.bfloat16))
