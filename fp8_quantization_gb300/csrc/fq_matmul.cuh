@@ -2072,9 +2072,10 @@ inline bool one_cta_tiles(int64_t rows, int64_t cols, int64_t groups, int64_t pa
 // that their HBM time hides no difference): rows of a tile of few rows (16, 32, 64), or
 // CTAs of a large tile (1, 2), whichever ends first by its time without blocks, that of
 // a block, and for few rows what more CTAs than SMs add, and each row whose sums come
-// from a cluster's CTAs.  Fitted to the five kernels' times at 200 sizes (1 to 2000 rows, dense
-// and in 4 to 32 groups, x 128 to 4096 columns, K 1024 to 7168): the choice is 0.7 % behind
-// the best of the five on average, 21 % at most.  64 x 2 x 896 x 7168: few rows 9.1 us, one CTA
+// from a cluster's CTAs.  Fitted to the five kernels' times at 14136 random sizes (1 to
+// 2500 rows, dense and in up to 64 groups, x 64 to 4096 columns, K 256 to 14336, every form
+// of the epilogue): the choice is 0.8 % behind the best of the five on average, 19 % at the
+// 99th percentile, and no more at 8742 others.  64 x 2 x 896 x 7168: few rows 9.1 us, one CTA
 // a tile 27.7; 100 x 1408 x 1024: 6.0, 8.6; 200 x 4096 x 7168: 22.5, 21.9.
 template <Epi kEpi>
 int pick_small(const MmArgs &p)
@@ -2106,17 +2107,17 @@ int pick_small(const MmArgs &p)
                       waves * ((p.KB + S - 1) / S) * block);
     };
     using std::integral_constant;
-    few(integral_constant<int, 16>{}, kTwo ? 3500 : 4250, kTwo ? 360 : 255, kTwo ? 1950 : 1100,
-        kTwo ? 275 : 185);
-    few(integral_constant<int, 32>{}, kTwo ? 5500 : 4800, kTwo ? 435 : 260, kTwo ? 3400 : 2450,
-        kTwo ? 270 : 180);
+    few(integral_constant<int, 16>{}, kTwo ? 3450 : 3500, kTwo ? 410 : 270, kTwo ? 1975 : 1025,
+        kTwo ? 280 : 310);
+    few(integral_constant<int, 32>{}, kTwo ? 4100 : 4600, kTwo ? 415 : 270, kTwo ? 2100 : 1270,
+        kTwo ? 290 : 225);
     if (!kTwo)
-        few(integral_constant<int, 64>{}, 4950, 465, 2200, 195);
+        few(integral_constant<int, 64>{}, 4800, 495, 875, 270);
     const int64_t wide = kTwo ? nt : (p.N + 255) / 256;
-    offer(1, (kTwo ? 6400 : 6600) +
-                 (row_tiles(128) * nt + sms - 1) / sms * p.KB * (kTwo ? 390 : 360));
-    offer(2, (kTwo ? 7150 : 9200) +
-                 (row_tiles(256) * wide + sms / 2 - 1) / (sms / 2) * p.KB * (kTwo ? 370 : 365));
+    offer(1, (kTwo ? 6800 : 7350) +
+                 (row_tiles(128) * nt + sms - 1) / sms * p.KB * (kTwo ? 390 : 247));
+    offer(2, (kTwo ? 8950 : 12050) +
+                 (row_tiles(256) * wide + sms / 2 - 1) / (sms / 2) * p.KB * (kTwo ? 370 : 397));
     return best;
 }
 

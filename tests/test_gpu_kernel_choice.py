@@ -44,3 +44,30 @@ def test_dense_gated_projections_of_large_weights(fq, M, F, K):
     ff.check("h", h, want, off + ff.rounded(want, torch.float32))
     ff.check("gate", z[:, 0], gate, dg + ff.rounded(gate, torch.bfloat16))
     ff.check("up", z[:, 1], up, du + ff.rounded(up, torch.bfloat16))
+
+
+@pytest.mark.parametrize("M,N,K,G", [(1003, 1001, 1408, 8), (418, 2688, 1152, 2), (246, 2432, 4992, 1),
+                                     (1096, 1497, 896, 7), (17, 300, 3584, 60)])
+def test_small_weights(fq, M, N, K, G):
+    """Every kind of epilogue where few rows, one CTA and pairs are close to one another."""
+    cut = torch.randint(0, M + 1, (G - 1,), generator=torch.Generator().manual_seed(K)).sort().values
+    bounds = [0, *cut.tolist(), M]
+    offs = torch.tensor(bounds, device="cuda")
+    y, ys, w, ws, gen = ff.make(M, N, K, G, 1, M + N, (2,))
+    gate, dg = ff.product(y, ys, w[:, 0], ws[:, 0], bounds)
+    up, du = ff.product(y, ys, w[:, 1], ws[:, 1], bounds)
+    a, _, da, _ = ff.act(gate, "gelu_tanh")
+    da = da + ff.SLOPE * dg
+    want = a * up
+    h = fq.fp8_matmul_gated(y, ys, w, ws, offs, act="gelu_tanh", out_dtype=torch.float32)
+    ff.check("h", h, want, da * (up.abs() + du) + a.abs() * du + ff.rounded(want, torch.float32))
+    one, ones = w[:, 0].contiguous(), ws[:, 0].contiguous()
+    z = torch.randn((M, 2, N), device="cuda", generator=gen).bfloat16()
+    dz = fq.fp8_matmul_act_backward(y, ys, one, ones, z, offs, out_dtype=torch.float32)
+    s, slope, ds, dslope = ff.act(z[:, 0], "silu")
+    v = z[:, 1].double()
+    want = gate * v * slope
+    ff.check("dgate", dz[:, 0], want, v.abs() * (dg * (slope.abs() + dslope) + gate.abs() * dslope)
+             + 2.0 ** -23 * want.abs() + ff.rounded(want, torch.float32))
+    want = gate * s
+    ff.check("dup", dz[:, 1], want, dg * (s.abs() + ds) + gate.abs() * ds + ff.rounded(want, torch.float32))
