@@ -33,7 +33,10 @@ constexpr int kMmThreads = (kPromoteWarps + 4) * 32;
 // 64512 = 256 x 200 + 128 x 104 = 256 x 208 + 128 x 88.  The other roles' spills
 // cost 10 to 20 % (at 56); with a scale per column the promoting warps need more
 // (with an epilogue they do not: act without options, 65536 x 2048 x 7168, 748 us at 200,
-// 779 at 208).
+// 779 at 208).  What is spilled all the same, bytes stored by -Xptxas -v, in tiles of pairs:
+// act up to 4, gated products 4 to 12 (up to 76 loaded, in the loop's scales), gradients 28 to
+// 60, gated gradients 28 to 32, and 144 to 148 with a scale per column (65536 x 2048 x 7168 with
+// h 2154 us, the plain activation's gradient 1379).
 constexpr int promote_regs(bool col_scale) { return col_scale ? 208 : 200; }
 constexpr int other_regs(bool col_scale) { return col_scale ? 88 : 104; }
 constexpr int kRaster = 8;        // row tiles walked together over the columns
@@ -282,8 +285,8 @@ __device__ __forceinline__ void add_bf16(const void *c, int64_t row_off, int32_t
 // predicates in it; what a tile at the end of a group or of the columns needs, or
 // rows that are not 16-byte aligned, is done at a step's begin and end, behind one
 // vote each; and all single-thread work is in elected blocks.  16384 x 7168 x 2048
-// with bias, silu, residual and z: 328 us, with silu alone 275; without any option
-// 222 (the plain product 197).
+// with bias, silu, residual and z: 335 us, with silu alone 281; without any option
+// 216 (the plain product 206 to 223).
 template <int kCtas, Mode kMode, Out kOut, Epi kEpi>
 struct Finish {
     using S = Shape<kCtas, kOut, kEpi>;
@@ -1936,7 +1939,6 @@ __global__ void __launch_bounds__(Few<kT, kEpi == kGated>::threads, Few<kT, kEpi
                             if (r < S)
                                 v[q] += of[r];
                     }
-                    const int64_t at = static_cast<int64_t>(row0 + e) * p.N + n;
                     if constexpr (kOut == kE4m3) {
                         float h, none, r, scale;
                         unpack2(fin.template gated<kSigmoid>(row0 + e, false, Act::both(v[0]),
@@ -1957,6 +1959,7 @@ __global__ void __launch_bounds__(Few<kT, kEpi == kGated>::threads, Few<kT, kEpi
                         fin.quantized(row0 + e, h, r);
                     } else if (n < p.N) {
                         if constexpr (kEpi == kPlain) {
+                            const int64_t at = static_cast<int64_t>(row0 + e) * p.N + n;
                             if (kOut == kF32)
                                 static_cast<float *>(p.c)[at] = v[0];
                             else

@@ -93,13 +93,15 @@ constexpr int kSumWarp = 32;   // up to so many rows: a warp
 constexpr int kSumShort = 64;
 // Rows of a partial sum.  65536 x 4096 BF16 in 32 groups, L2 flushed: 256 rows 110 us,
 // 512 108, 1024 106; 16384 x 2048 in 8: 25.2, 28.3, 35.5; 4096 x 1024: 15.0, 21.2, 30.4.
-// So long pieces, but shorter ones where every SM would not have four; 55482 x 144 FP32 in
-// one group: 128 rows 18.6 (the join), 512 14.0.
+// So long pieces, but shorter ones where each of the 152 SMs would not have four (a number, not
+// the current device's: the workspace's size does not depend on where it is asked for);
+// 55482 x 144 FP32 in one group: 128 rows 18.6 (the join), 512 14.0.
+constexpr int64_t kSumMany = 4 * 152;
 constexpr int32_t sum_rows(int64_t M, int64_t N)
 {
     if (M <= 16384)
         return 128;
-    return M / 512 * ((N + kSumCols - 1) / kSumCols) >= 608 ? 512 : 256;
+    return M / 512 * ((N + kSumCols - 1) / kSumCols) >= kSumMany ? 512 : 256;
 }
 
 // What the threads before this one hold, added up, and (all) what all hold.
@@ -227,7 +229,8 @@ __device__ __forceinline__ void sum_columns(const T *__restrict__ x, int32_t lo,
 // most pieces are short (kShort), what a CTA costs before its first row is what counts: a
 // grid that fits at once, where a warp takes a piece of up to kSumWarp rows and a CTA only
 // the longer ones.  4096 x 7168 BF16 in 256 groups 17 us, a CTA a piece 92; 1024 rows in
-// 1024 groups 11, 1028.
+// 1024 groups 11, 1028.  Four CTAs an SM leave 64 registers, and spills of 16 bytes for BF16,
+// 24 with kShort, 56 to 152 where rows are not aligned.
 template <typename T, bool kVec, int kWarps, bool kShort>
 __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 4 : 1) group_sum_part_kernel(
     const T *__restrict__ x, int32_t M, int64_t N, const int64_t *__restrict__ offs, int32_t G,
